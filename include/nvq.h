@@ -234,6 +234,46 @@ nvq_status nvfp4_gemm_w4a4_swiglu(const uint8_t* x_codes, const uint8_t* x_scale
                                   int64_t K, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * Bias, activation and residual in the epilogue of a product:
+ *
+ *   y[m, n] = bf16_RNE( act(v[m, n] + bias[n]) + residual[m, n] )
+ *
+ * with v the FP32 product and everything up to the one rounding in FP32.
+ *   NVQ_ACT_RELU       max(z, 0)  (NaN stays NaN)
+ *   NVQ_ACT_GELU       z (1 + erf(z / sqrt 2)) / 2
+ *   NVQ_ACT_GELU_TANH  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
+ *   NVQ_ACT_SILU       z / (1 + exp(-z))
+ * bias_bf16        [N] BF16 or NULL, 16-byte aligned.
+ * residual_bf16    [M, N] BF16 or NULL, 16-byte aligned.  It may be y itself
+ *                  (the same pointer and stride: the residual stream is updated
+ *                  in place), or hold other columns of the same buffer; any
+ *                  other overlap with y is NVQ_ERR_INVALID_ARG.
+ * residual_stride, y_stride: elements from one row to the next, >= N and a
+ *                  multiple of 8; 0 means N.
+ * A NULL nvq_epilogue* (or one of all zeros) is the bare product.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  NVQ_ACT_NONE = 0,
+  NVQ_ACT_RELU = 1,
+  NVQ_ACT_GELU = 2,
+  NVQ_ACT_GELU_TANH = 3,
+  NVQ_ACT_SILU = 4
+} nvq_activation;
+typedef struct {
+  const void* bias_bf16;
+  const void* residual_bf16;
+  int64_t residual_stride;
+  int64_t y_stride;
+  int activation; /* an nvq_activation */
+} nvq_epilogue;
+
+/* nvfp4_gemm_w4a4 with an epilogue: arguments and shape rules as there. */
+nvq_status nvfp4_gemm_w4a4_epilogue(const uint8_t* x_codes, const uint8_t* x_scales, const float* t_x,
+                                    const uint8_t* w_codes, const uint8_t* w_scales, const float* t_w,
+                                    void* y_bf16, int64_t M, int64_t N, int64_t K,
+                                    const nvq_epilogue* epilogue, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * INT4 group-128 round-to-nearest weight quantization (MARLIN page: 4-bit
  * weights with one scale per 128-weight group).
  *
@@ -307,6 +347,14 @@ nvq_status w4a16_gemm(const void* x_bf16, const uint8_t* packed_codes, const voi
                       void* y_bf16, int64_t M, int64_t N, int64_t K,
                       void* workspace, size_t workspace_bytes, void* stream);
 
+/* w4a16_gemm with an epilogue: arguments, shape rules and launch behaviour as
+ * there (bias and residual are read after the wait on the preceding kernel; an
+ * in-place residual is read once, also in calls of several passes).  x may not
+ * overlap y. */
+nvq_status w4a16_gemm_epilogue(const void* x_bf16, const uint8_t* packed_codes, const void* packed_scales,
+                               void* y_bf16, int64_t M, int64_t N, int64_t K, const nvq_epilogue* epilogue,
+                               void* stream);
+
 /* ------------------------------------------------------------------------ *
  * 2:4-sparse INT4 decode (MARLIN page, abeam.tech: its official implementation
  * also combines the group-128 INT4 weights with 2:4 structured sparsity).
@@ -362,6 +410,14 @@ nvq_status nvq_linear(const void* x_bf16, int64_t M, int64_t N, int64_t K,
                       const uint8_t* w_packed_codes, const void* w_packed_scales,
                       int64_t crossover_m, void* y_bf16, void* workspace, size_t workspace_bytes,
                       void* stream);
+
+/* nvq_linear with an epilogue: the same choice of path, workspace and rules;
+ * the product is w4a16_gemm_epilogue or nvfp4_gemm_w4a4_epilogue. */
+nvq_status nvq_linear_epilogue(const void* x_bf16, int64_t M, int64_t N, int64_t K,
+                               const uint8_t* w_codes, const uint8_t* w_scales, const float* w_t,
+                               const uint8_t* w_packed_codes, const void* w_packed_scales,
+                               int64_t crossover_m, void* y_bf16, const nvq_epilogue* epilogue,
+                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ *
  * Prefill over layers whose NVFP4 weights live in pinned host memory

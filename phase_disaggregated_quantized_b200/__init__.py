@@ -11,10 +11,12 @@ Prefill (Mix-Quant page, gist.science, section 2): ``nvfp4_quantize`` then
 ``nvfp4_gemm_w4a4``.  Decode (MARLIN page, abeam.tech): ``int4_quantize`` and
 ``int4_pack_weights`` offline, then ``w4a16_gemm``.  ``nvq_linear`` picks one
 of the two by the batch size M (Disaggregated Quantization page,
-singularity-lens.com: one master weight kept in both formats).
+singularity-lens.com: one master weight kept in both formats).  The calls
+ending in ``_epilogue`` add bias, activation and residual to those products.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -36,6 +38,15 @@ class StreamLayer(ctypes.Structure):
     _fields_ = [("w_codes_host", ctypes.c_void_p), ("w_scales_host", ctypes.c_void_p),
                 ("w_t_host", ctypes.c_void_p), ("x_bf16", ctypes.c_void_p), ("y_bf16", ctypes.c_void_p),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64)]
+
+
+class Epilogue(ctypes.Structure):
+    """nvq_epilogue of include/nvq.h."""
+    _fields_ = [("bias_bf16", ctypes.c_void_p), ("residual_bf16", ctypes.c_void_p),
+                ("residual_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("activation", ctypes.c_int)]
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
 class NvqError(RuntimeError):
@@ -76,6 +87,10 @@ def lib() -> ctypes.CDLL:
             "nvfp4_scale_from_amax": ([vp, vp, vp], i32),
             "nvfp4_gemm_w4a4": ([vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp], i32),
             "nvfp4_gemm_w4a4_swiglu": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp], i32),
+            "nvfp4_gemm_w4a4_epilogue": ([vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, ctypes.POINTER(Epilogue), vp], i32),
+            "w4a16_gemm_epilogue": ([vp, vp, vp, vp, i64, i64, i64, ctypes.POINTER(Epilogue), vp], i32),
+            "nvq_linear_epilogue": ([vp, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp, ctypes.POINTER(Epilogue), vp, sz,
+                                     vp], i32),
             "int4_quantize": ([vp, i64, i64, vp, vp, vp], i32),
             "int4_pack_weights": ([vp, vp, i64, i64, vp, vp, vp], i32),
             "w4a16_workspace_bytes": ([i64, i64, i64], sz),
@@ -362,6 +377,142 @@ def nvq_linear(x, w4a4=None, w4a16=None, N: int | None = None, *, crossover_m: i
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().nvq_linear(_ptr(x), M, N, K, _ptr(wc), _ptr(wsc), _ptr(wt), _ptr(pc), _ptr(ps), crossover_m,
                             _ptr(y), _ptr(workspace), ws_bytes, _stream(stream)), "nvq_linear")
+    return y
+
+
+# ------------------------------------------------------------------ products with an epilogue
+def _on(dev, stream):
+    """The context of one call on tensors of `dev`: that device current and, when the
+    caller names a stream, what the call allocates belonging to that stream."""
+    if stream is None:
+        return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _need(t, name, dev, dtype, shape=None, numel=None):
+    """A contiguous tensor of this type and size on the call's device."""
+    if t.device != dev or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {dev}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if numel is not None and t.numel() * t.element_size() < numel:
+        raise ValueError(f"{name} must hold at least {numel} bytes")
+
+
+def _need_rows(t, name, dev, M, N):
+    """A BF16 [M, N] tensor with contiguous rows; returns its row stride (0: N)."""
+    if t.device != dev or t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] != M or t.shape[1] != N:
+        raise ValueError(f"{name} must be a [{M}, {N}] bfloat16 tensor on {dev}")
+    if M <= 1 and (N <= 1 or t.stride(1) == 1):
+        return 0
+    if t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0)
+
+
+def _cuda_device(x, name):
+    if not x.is_cuda:
+        raise ValueError(f"libnvq calls take CUDA tensors ({name})")
+    return x.device
+
+
+def _epilogue(dev, M, N, bias, activation, residual, y):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
+    e = Epilogue()
+    if bias is not None:
+        _need(bias, "bias", dev, torch.bfloat16, shape=(N,))
+        e.bias_bf16 = bias.data_ptr()
+    if residual is not None:
+        e.residual_stride = _need_rows(residual, "residual", dev, M, N)
+        e.residual_bf16 = residual.data_ptr()
+    e.y_stride = _need_rows(y, "y", dev, M, N)
+    e.activation = ACTIVATIONS[activation]
+    return e
+
+
+def nvfp4_gemm_w4a4_epilogue(xq, wq, M: int, N: int, K: int, *, bias=None, activation: str = "none", residual=None,
+                             y=None, stream=None):
+    """Y [M, N] bf16 = act(dequant(xq) @ dequant(wq)^T + bias) + residual.
+
+    xq / wq: (codes, scales, t) of nvfp4_quantize.  bias: [N] bf16; activation:
+    a name of ACTIVATIONS; residual: [M, N] bf16.  residual and y may be views
+    with contiguous rows (a row stride that is a multiple of 8), and residual
+    may be y: the residual stream updated in place."""
+    xc, xs, tx = xq
+    wc, ws, tw = wq
+    dev = _cuda_device(xc, "xq")
+    for name, (c, s, t), rows in (("xq", xq, M), ("wq", wq, N)):
+        _need(c, name + " codes", dev, torch.uint8, numel=rows * (K // 2))
+        _need(s, name + " scales", dev, torch.uint8, numel=nvfp4_scales_bytes(rows, K))
+        _need(t, name + " t", dev, torch.float32, numel=4)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        e = _epilogue(dev, M, N, bias, activation, residual, y)
+        _check(lib().nvfp4_gemm_w4a4_epilogue(xc.data_ptr(), xs.data_ptr(), tx.data_ptr(), wc.data_ptr(),
+                                              ws.data_ptr(), tw.data_ptr(), y.data_ptr(), M, N, K, ctypes.byref(e),
+                                              _stream(stream)), "nvfp4_gemm_w4a4_epilogue")
+    return y
+
+
+def w4a16_gemm_epilogue(x, packed_codes, packed_scales, N: int, *, bias=None, activation: str = "none",
+                        residual=None, y=None, stream=None):
+    """Y [M, N] bf16 = act(X W^T + bias) + residual for packed INT4 W [N, K]
+    (int4_pack_weights).  bias, activation, residual, y as in
+    nvfp4_gemm_w4a4_epilogue; x may not overlap y."""
+    dev = _cuda_device(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    _need(x, "x", dev, torch.bfloat16)
+    _need(packed_codes, "packed_codes", dev, torch.uint8, numel=N * K // 2)
+    _need(packed_scales, "packed_scales", dev, torch.uint8, numel=N * (K // 128) * 2)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        e = _epilogue(dev, M, N, bias, activation, residual, y)
+        _check(lib().w4a16_gemm_epilogue(x.data_ptr(), packed_codes.data_ptr(), packed_scales.data_ptr(),
+                                         y.data_ptr(), M, N, K, ctypes.byref(e), _stream(stream)),
+               "w4a16_gemm_epilogue")
+    return y
+
+
+def nvq_linear_epilogue(x, w4a4=None, w4a16=None, N: int | None = None, *, bias=None, activation: str = "none",
+                        residual=None, crossover_m: int = -1, y=None, workspace=None, stream=None):
+    """nvq_linear with bias, activation and residual in the product it picks."""
+    dev = _cuda_device(x, "x")
+    if N is None:
+        raise ValueError("N is required")
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    _need(x, "x", dev, torch.bfloat16)
+    w = [None] * 5
+    if w4a4 is not None:
+        for t, name, dt, n in zip(w4a4, ("codes", "scales", "t"), (torch.uint8, torch.uint8, torch.float32),
+                                  (N * (K // 2), nvfp4_scales_bytes(N, K), 4)):
+            _need(t, "w4a4 " + name, dev, dt, numel=n)
+        w[:3] = (t.data_ptr() for t in w4a4)
+    if w4a16 is not None:
+        for t, name, n in zip(w4a16, ("codes", "scales"), (N * K // 2, N * (K // 128) * 2)):
+            _need(t, "w4a16 " + name, dev, torch.uint8, numel=n)
+        w[3:] = (t.data_ptr() for t in w4a16)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        need = nvq_linear_workspace_bytes(M, N, K, crossover_m)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = 0
+        if workspace is not None:
+            _need(workspace, "workspace", dev, workspace.dtype)
+            ws_bytes = workspace.numel() * workspace.element_size()
+        e = _epilogue(dev, M, N, bias, activation, residual, y)
+        _check(lib().nvq_linear_epilogue(x.data_ptr(), M, N, K, *w, crossover_m, y.data_ptr(), ctypes.byref(e),
+                                         _ptr(workspace), ws_bytes, _stream(stream)), "nvq_linear_epilogue")
     return y
 
 

@@ -34,6 +34,7 @@
 // 32c + lane) and B scales at 16 + 8j .. 16 + 8j + 7 (column c: rows 32c + lane),
 // the same in all four sub-partitions.
 #pragma once
+#include "epilogue.cuh"
 #include "nvfp4_quantize.cuh"
 #include "ptx.cuh"
 
@@ -63,8 +64,8 @@ constexpr int OFF_C = OFF_B + STAGES * B_BYTES;
 constexpr int OFF_SFA = OFF_C + EPI_WARPS * C_BYTES;
 constexpr int OFF_SFB = OFF_SFA + STAGES * SFA_BYTES;
 constexpr int OFF_BAR = OFF_SFB + STAGES * SFB_BYTES;
-// full[S], empty[S], acc_full[2], acc_empty[2], overlap_free, sf_full[2], drain, scales_in[S]
-constexpr int NUM_BARS = 2 * STAGES + 2 + 2 + 1 + SF_SLOTS + 1 + STAGES;
+// full[S], empty[S], acc_full[2], acc_empty[2], overlap_free, sf_full[2], drain, scales_in[S], residual[8]
+constexpr int NUM_BARS = 2 * STAGES + 2 + 2 + 1 + SF_SLOTS + 1 + STAGES + EPI_WARPS;
 constexpr int OFF_TMEM_PTR = OFF_BAR + NUM_BARS * 8;
 constexpr int SMEM_BYTES = OFF_TMEM_PTR + 16 + 1024;    // + slack for 1024-byte alignment
 static_assert(SMEM_BYTES <= 232448, "smem budget");
@@ -89,6 +90,8 @@ struct Params {
   uint8_t* h_scales;       // tiled E4M3 scales of H, padded rows zero
   const float* t_h;        // static tensor scale of H
   uint32_t h_katoms;       // (N / 2) / 64
+  // Bias, activation, residual epilogue only (the residual comes through its own tensor map)
+  EpiParams epi;
 };
 
 // Tile order: the tiles in flight at once (one per SM) cover a band of tiles
@@ -213,10 +216,13 @@ __device__ __forceinline__ uint32_t acc_col(uint32_t buf) { return buf ? ACC1_CO
 
 // EPI 0: Y = BF16(alpha acc).  EPI 1: B rows interleaved in blocks of 128 (gate,
 // up, gate, up, ...); H = silu(gate) * up quantized to NVFP4 with a static t_h.
+// EPI 2: Y = BF16(act(alpha acc + bias) + residual), Y and the residual with
+// row strides of their own.
 template <int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
 nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                  const __grid_constant__ CUtensorMap tmap_y, const Params p) {
+                  const __grid_constant__ CUtensorMap tmap_y, const __grid_constant__ CUtensorMap tmap_r,
+                  const Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_addr(smem);
@@ -229,6 +235,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
   const uint32_t bar_sf_full = bar_overlap + 8;               // + 8 slot
   const uint32_t bar_drain = bar_sf_full + 8 * SF_SLOTS;
   const uint32_t bar_sc_in = bar_drain + 8;                   // + 8 s: the stage's scale atoms landed
+  const uint32_t bar_res = bar_sc_in + 8 * STAGES;            // + 8 w: epilogue warp w's residual chunk landed (EPI 2)
   uint32_t* tmem_ptr_smem = reinterpret_cast<uint32_t*>(smem + OFF_TMEM_PTR);
 
   if (threadIdx.x == 0) {
@@ -246,10 +253,13 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       mbar_init(bar_sf_full + 8 * k, 4);                      // one arrive per scale-writer warp
     }
     mbar_init(bar_drain, 1);
+    if (EPI == 2)
+      for (int w = 0; w < EPI_WARPS; ++w) mbar_init(bar_res + 8 * w, 1);
     fence_mbar_init();
     prefetch_tensormap(&tmap_a);
     prefetch_tensormap(&tmap_b);
-    if (EPI == 0) prefetch_tensormap(&tmap_y);
+    if (EPI != 1) prefetch_tensormap(&tmap_y);
+    if (EPI == 2 && p.epi.residual != nullptr) prefetch_tensormap(&tmap_r);
   }
   if (warp == 0) {
     tmem_alloc(smem_addr(tmem_ptr_smem), TMEM_COLS);
@@ -465,6 +475,118 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       }
     }
     if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+    (void)row;
+    } else if constexpr (EPI == 2) {
+    // As EPI 0, with each 32 x 64 chunk of the residual loaded by TMA into the
+    // warp's staging buffer (where the result then replaces it): the tile's
+    // first chunk while the accumulator is still being computed, the second
+    // once the first one's store has read the buffer.
+    uint8_t* cbuf = smem + OFF_C + (warp - 2) * C_BYTES;
+    const uint32_t cbuf_s = smem_addr(cbuf);
+    const uint32_t rbar = bar_res + 8 * (warp - 2);
+    const bool has_res = p.epi.residual != nullptr;
+    uint64_t pol = 0;
+    if (has_res && lane == 0) pol = policy_evict_first();
+    uint32_t acc_par = 0, local = 0, rphase = 0;
+    bool dead = false, pending = false;                       // pending: a residual load not yet waited for
+    // Warp-uniform: the chunk at (col0, row0) of the residual, unless it lies outside Y.
+    auto request = [&](uint32_t col0, uint32_t row0) {
+      if (!has_res || col0 >= p.N || row0 >= p.M) return;
+      if (lane == 0) {
+        bulk_wait_read<0>();                                  // the previous store has read the buffer
+        mbar_arrive_expect_tx(rbar, C_BYTES);
+        tma_load_2d(cbuf_s, &tmap_r, rbar, (int)col0, (int)row0, pol);
+      }
+      pending = true;
+      __syncwarp();
+    };
+    auto first_chunk = [&](uint32_t b) { return (b ? 0u : 2u) + h; };
+    if (blockIdx.x < num_tiles) {
+      uint32_t mt, nt;
+      tile_coords(blockIdx.x, p, mt, nt);
+      request(nt * BN + first_chunk(0) * C_COLS, mt * BM + q * 32);
+    }
+    for (uint32_t tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++local) {
+      uint32_t mt, nt;
+      tile_coords(tile, p, mt, nt);
+      const uint32_t buf = local & 1u;
+      if (!dead && !warp_mbar_wait(bar_acc_full + 8 * buf, (acc_par >> buf) & 1u)) dead = true;
+      acc_par ^= 1u << buf;
+      if (dead) continue;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((q * 32u) << 16) + acc_col(buf);
+      const uint32_t ch_first = first_chunk(buf), ch_second = (buf ? 2u : 0u) + h;
+      const uint32_t row0 = mt * BM + q * 32;
+      uint32_t v[64];
+      tc_ld_32x32b_x64(taddr + ch_first * C_COLS, v);
+      tc_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_overlap);
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        const uint32_t col0 = nt * BN + (part ? ch_second : ch_first) * C_COLS;
+        const bool inside = col0 < p.N && row0 < p.M;
+        if (part == 1 && !dead) request(col0, row0);
+        bool res = pending && !dead;                          // this chunk's residual
+        if (res) {
+          if (warp_mbar_wait(rbar, rphase)) {
+            pending = false;
+            rphase ^= 1u;
+          } else {
+            dead = true;
+            res = false;
+          }
+        } else {
+          if (lane == 0) bulk_wait_read<0>();                 // previous store done reading staging
+          __syncwarp();
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * e + i]) * alpha;
+          if (p.epi.bias != nullptr && col0 + 8 * e < p.N) {   // N % 8 == 0
+            const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.epi.bias + col0 + 8 * e));
+            f[0] += bf16_lo(b.x); f[1] += bf16_hi(b.x); f[2] += bf16_lo(b.y); f[3] += bf16_hi(b.y);
+            f[4] += bf16_lo(b.z); f[5] += bf16_hi(b.z); f[6] += bf16_lo(b.w); f[7] += bf16_hi(b.w);
+          }
+          activate(f, p.epi.act);
+          // 128-byte swizzle: 16-byte chunk e of row r sits at chunk e ^ (r & 7).
+          uint4* cell = reinterpret_cast<uint4*>(cbuf + lane * 128u + ((uint32_t)e ^ (lane & 7u)) * 16u);
+          if (res) {
+            const uint4 r = *cell;
+            f[0] += bf16_lo(r.x); f[1] += bf16_hi(r.x); f[2] += bf16_lo(r.y); f[3] += bf16_hi(r.y);
+            f[4] += bf16_lo(r.z); f[5] += bf16_hi(r.z); f[6] += bf16_lo(r.w); f[7] += bf16_hi(r.w);
+          }
+          *cell = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                             pack_bf16x2(f[6], f[7]));
+        }
+        if (part == 0) tc_ld_32x32b_x64(taddr + ch_second * C_COLS, v);   // in flight during the store
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && inside && !dead) {
+          tma_store_2d(&tmap_y, cbuf_s, (int)col0, (int)row0);
+          bulk_commit();
+        }
+        if (part == 0) {
+          tc_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_acc_empty + 8 * buf);   // all of this tile's TMEM read
+        }
+      }
+      const uint32_t next = tile + gridDim.x;
+      if (next < num_tiles && !dead) {
+        tile_coords(next, p, mt, nt);
+        request(nt * BN + first_chunk(buf ^ 1u) * C_COLS, mt * BM + q * 32);
+      }
+    }
+    if (lane == 0) {
+      if (pending) mbar_wait_drain(rbar, rphase, 200000000ull);   // a load in flight lands before the CTA exits
+      bulk_wait<0>();
+    }
     __syncwarp();
     (void)row;
     } else {

@@ -104,11 +104,11 @@ bool gemm_tiles_fit(int64_t M, int64_t N) { return ((M + 127) / 128) * ((N + 127
 // tiles (32 weight rows dense, 16 for 2:4 sparse).  Batch rows are handled 8 * NT8 at a time.
 constexpr int kMaxDevices = 64;
 
-template <int NT8, bool SPARSE = false>
+template <int NT8, bool SPARSE = false, bool EPI = false>
 nvq_status launch_w4a16(const void* x, const uint8_t* pc, const void* ps, void* y, int64_t M, int64_t N, int64_t K,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, const nvq::EpiParams& ep = {}) {
   using C = nvq::w4a16::Cfg<NT8, SPARSE>;
-  auto fn = nvq::w4a16::w4a16_kernel<NT8, SPARSE>;
+  auto fn = nvq::w4a16::w4a16_kernel<NT8, SPARSE, EPI>;
   static std::atomic<int> max_clusters[kMaxDevices];   // 0: not queried yet on that device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -142,7 +142,7 @@ nvq_status launch_w4a16(const void* x, const uint8_t* pc, const void* ps, void* 
   cfg.gridDim = dim3((unsigned)(nclu * nvq::w4a16::CS), 1, 1);
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, fn, static_cast<const __nv_bfloat16*>(x), pc, static_cast<const uint8_t*>(ps),
-                         static_cast<__nv_bfloat16*>(y), (uint32_t)M, (uint32_t)N, (uint32_t)K);
+                         static_cast<__nv_bfloat16*>(y), (uint32_t)M, (uint32_t)N, (uint32_t)K, ep);
   if (e != cudaSuccess) return cuda_fail(e, "w4a16_kernel launch");
   return launch_status("w4a16_kernel");
 }
@@ -199,6 +199,57 @@ StreamWs stream_ws_layout(const nvq_stream_layer* layers, int n, int64_t M) {
   W.total = W.act + W.act_scratch_off + W.act_scratch_bytes;
   W.ok = true;
   return W;
+}
+
+// First and one past the last byte of an [M, N] BF16 matrix with row stride ld.
+struct Span {
+  uintptr_t lo, hi;
+};
+Span bf16_span(const void* p, int64_t M, int64_t N, int64_t ld) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + 2 * ((uintptr_t)(M - 1) * (uintptr_t)ld + (uintptr_t)N)};
+}
+bool spans_meet(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Whether `a` may be read while y is written element by element: the same
+// matrix, or no element in common (disjoint, or other columns of the same rows).
+bool may_alias_y(const void* a, int64_t lda, const void* y, int64_t ldy, int64_t M, int64_t N) {
+  if (a == y && (lda == ldy || M == 1)) return true;
+  if (!spans_meet(bf16_span(a, M, N, lda), bf16_span(y, M, N, ldy))) return true;
+  if (lda != ldy) return false;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), py = reinterpret_cast<uintptr_t>(y);
+  const uintptr_t off = ((pa > py ? pa - py : py - pa) / 2) % (uintptr_t)ldy;
+  return off >= (uintptr_t)N && off + (uintptr_t)N <= (uintptr_t)ldy;
+}
+
+// The epilogue arguments of one product (M > 0, N > 0 and y checked before).
+nvq_status epilogue_params(const char* name, const nvq_epilogue* e, const void* y, int64_t M, int64_t N,
+                           nvq::EpiParams* out) {
+  char msg[160];
+  auto bad = [&](nvq_status s, const char* what) {
+    snprintf(msg, sizeof(msg), "%s: %s", name, what);
+    return fail(s, msg);
+  };
+  *out = nvq::EpiParams{};
+  out->ldr = out->ldy = (size_t)N;
+  if (e == nullptr) return NVQ_OK;
+  if (e->activation < NVQ_ACT_NONE || e->activation > NVQ_ACT_SILU) return bad(NVQ_ERR_INVALID_ARG, "unknown activation");
+  const int64_t ldy = e->y_stride == 0 ? N : e->y_stride;
+  const int64_t ldr = e->residual_stride == 0 ? N : e->residual_stride;
+  if (ldy < N || (e->residual_bf16 && ldr < N)) return bad(NVQ_ERR_INVALID_ARG, "row stride below N");
+  if (ldy % 8 != 0 || (e->residual_bf16 && ldr % 8 != 0)) return bad(NVQ_ERR_MISALIGNED, "row stride not a multiple of 8");
+  if (ldy >= kMaxDim || ldr >= kMaxDim) return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "row stride too large");
+  if (!aligned16(e->bias_bf16) || !aligned16(e->residual_bf16)) return bad(NVQ_ERR_MISALIGNED, "bias or residual not 16-byte aligned");
+  if (e->residual_bf16 && !may_alias_y(e->residual_bf16, ldr, y, ldy, M, N))
+    return bad(NVQ_ERR_INVALID_ARG, "residual overlaps y without being y");
+  if (e->bias_bf16 && spans_meet(bf16_span(e->bias_bf16, 1, N, N), bf16_span(y, M, N, ldy)))
+    return bad(NVQ_ERR_INVALID_ARG, "bias lies inside y");
+  out->bias = static_cast<const __nv_bfloat16*>(e->bias_bf16);
+  out->residual = static_cast<const __nv_bfloat16*>(e->residual_bf16);
+  out->ldr = (size_t)ldr;
+  out->ldy = (size_t)ldy;
+  out->act = (uint32_t)e->activation;
+  return NVQ_OK;
 }
 
 }  // namespace
@@ -428,20 +479,27 @@ nvq_status nvfp4_scale_from_amax(const float* amax, float* tensor_scale_out, voi
 namespace {
 
 // EPI 0: y_bf16 receives Y.  EPI 1: h_* receive NVFP4(silu(gate) * up) with the
-// static scale t_h (B rows interleaved in blocks of 128: gate, up, ...).
+// static scale t_h (B rows interleaved in blocks of 128: gate, up, ...).  EPI 2:
+// y_bf16 receives act(Y + bias) + residual, row strides in epi.
 template <int EPI>
 nvq_status launch_w4a4(const uint8_t* x_codes, const uint8_t* x_scales, const float* t_x, const uint8_t* w_codes,
                        const uint8_t* w_scales, const float* t_w, void* y_bf16, int64_t M, int64_t N, int64_t K,
-                       uint8_t* h_codes, uint8_t* h_scales, const float* t_h, cudaStream_t stream) {
+                       uint8_t* h_codes, uint8_t* h_scales, const float* t_h, cudaStream_t stream,
+                       const nvq::EpiParams& epi = {}) {
   using namespace nvq::w4a4;
-  CUtensorMap ma, mb, my;
+  CUtensorMap ma, mb, my, mr;
   memset(&my, 0, sizeof(my));                               // EPI 1 never touches Y
+  memset(&mr, 0, sizeof(mr));                               // the residual: EPI 2 only
+  const uint64_t ldy = EPI == 2 ? (uint64_t)epi.ldy : (uint64_t)N;
   if (!make_map_2d(&ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_codes, (uint64_t)K / 2, (uint64_t)M, (uint64_t)K / 2,
                    BKB, BM) ||
       !make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, (uint64_t)K / 2, (uint64_t)N, (uint64_t)K / 2,
                    BKB, BN) ||
-      (EPI == 0 && !make_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y_bf16, (uint64_t)N, (uint64_t)M,
-                                (uint64_t)N * 2, C_COLS, 32)))   // one epilogue warp: 32 rows x 64 columns
+      (EPI != 1 && !make_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y_bf16, (uint64_t)N, (uint64_t)M,
+                                ldy * 2, C_COLS, 32)) ||         // one epilogue warp: 32 rows x 64 columns
+      (EPI == 2 && epi.residual != nullptr &&
+       !make_map_2d(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, epi.residual, (uint64_t)N, (uint64_t)M,
+                    (uint64_t)epi.ldr * 2, C_COLS, 32)))
     return fail(NVQ_ERR_CUDA, "nvfp4_gemm_w4a4: tensor map encoding failed");
   Params p;
   p.x_scales = x_scales;
@@ -462,6 +520,7 @@ nvq_status launch_w4a4(const uint8_t* x_codes, const uint8_t* x_scales, const fl
   p.h_scales = h_scales;
   p.t_h = t_h;
   p.h_katoms = (uint32_t)(N / 2 / 64);
+  p.epi = epi;
   // The shared-memory opt-in is a per-device setting of the kernel: once per device.
   int dev = 0;
   const cudaError_t de = cudaGetDevice(&dev);
@@ -476,7 +535,7 @@ nvq_status launch_w4a4(const uint8_t* x_codes, const uint8_t* x_scales, const fl
   if (attr_err[dev] != cudaSuccess) return cuda_fail(attr_err[dev], "nvfp4_gemm_w4a4: smem attribute");
   const uint64_t tiles = (uint64_t)p.num_m_tiles * p.num_n_tiles;
   const int grid = (int)std::min<uint64_t>(tiles, (uint64_t)sm_count());
-  nvfp4_gemm_kernel<EPI><<<grid, THREADS, SMEM_BYTES, stream>>>(ma, mb, my, p);
+  nvfp4_gemm_kernel<EPI><<<grid, THREADS, SMEM_BYTES, stream>>>(ma, mb, my, mr, p);
   return launch_status("nvfp4_gemm_kernel");
 }
 
@@ -521,6 +580,28 @@ nvq_status nvfp4_gemm_w4a4_swiglu(const uint8_t* x_codes, const uint8_t* x_scale
   if (M == 0) return NVQ_OK;
   return launch_w4a4<1>(x_codes, x_scales, t_x, w_codes, w_scales, t_w, nullptr, M, N, K, h_codes, h_scales, t_h,
                         stream);
+}
+
+nvq_status nvfp4_gemm_w4a4_epilogue(const uint8_t* x_codes, const uint8_t* x_scales, const float* t_x,
+                                    const uint8_t* w_codes, const uint8_t* w_scales, const float* t_w, void* y_bf16,
+                                    int64_t M, int64_t N, int64_t K, const nvq_epilogue* epilogue, void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (M < 0 || N <= 0 || K <= 0) return fail(NVQ_ERR_INVALID_ARG, "nvfp4_gemm_w4a4_epilogue: bad sizes");
+  if (N % 8 != 0 || K % 64 != 0)
+    return fail(NVQ_ERR_UNSUPPORTED_SHAPE, "nvfp4_gemm_w4a4_epilogue: need N % 8 == 0, K % 64 == 0");
+  if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim || !gemm_tiles_fit(M, N))
+    return fail(NVQ_ERR_UNSUPPORTED_SHAPE, "nvfp4_gemm_w4a4_epilogue: too large");
+  if (!x_codes || !x_scales || !t_x || !w_codes || !w_scales || !t_w || !y_bf16)
+    return fail(NVQ_ERR_INVALID_ARG, "nvfp4_gemm_w4a4_epilogue: NULL pointer");
+  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
+      !aligned16(y_bf16) || (reinterpret_cast<uintptr_t>(t_x) & 3u) || (reinterpret_cast<uintptr_t>(t_w) & 3u))
+    return fail(NVQ_ERR_MISALIGNED, "nvfp4_gemm_w4a4_epilogue: pointer not aligned");
+  if (M == 0) return NVQ_OK;
+  nvq::EpiParams ep;
+  const nvq_status st = epilogue_params("nvfp4_gemm_w4a4_epilogue", epilogue, y_bf16, M, N, &ep);
+  if (st != NVQ_OK) return st;
+  return launch_w4a4<2>(x_codes, x_scales, t_x, w_codes, w_scales, t_w, y_bf16, M, N, K, nullptr, nullptr, nullptr,
+                        stream, ep);
 }
 
 // ------------------------------------------------------------------ INT4
@@ -587,6 +668,30 @@ nvq_status w4a16_gemm(const void* x_bf16, const uint8_t* packed_codes, const voi
   if (M <= 8) return launch_w4a16<1>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream);
   if (M <= 16) return launch_w4a16<2>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream);
   return launch_w4a16<4>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream);
+}
+
+nvq_status w4a16_gemm_epilogue(const void* x_bf16, const uint8_t* packed_codes, const void* packed_scales,
+                               void* y_bf16, int64_t M, int64_t N, int64_t K, const nvq_epilogue* epilogue,
+                               void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (M < 0 || N <= 0 || K <= 0) return fail(NVQ_ERR_INVALID_ARG, "w4a16_gemm_epilogue: bad sizes");
+  if (N % 32 != 0 || K % 128 != 0)
+    return fail(NVQ_ERR_UNSUPPORTED_SHAPE, "w4a16_gemm_epilogue: need N % 32 == 0, K % 128 == 0");
+  if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim || (N / 32) * (K / 128) >= ((int64_t)1 << 32))
+    return fail(NVQ_ERR_UNSUPPORTED_SHAPE, "w4a16_gemm_epilogue: too large");
+  if (M == 0) return NVQ_OK;
+  if (!x_bf16 || !packed_codes || !packed_scales || !y_bf16)
+    return fail(NVQ_ERR_INVALID_ARG, "w4a16_gemm_epilogue: NULL pointer");
+  if (!aligned16(x_bf16) || !aligned16(packed_codes) || !aligned16(packed_scales) || !aligned16(y_bf16))
+    return fail(NVQ_ERR_MISALIGNED, "w4a16_gemm_epilogue: pointer not 16-byte aligned");
+  nvq::EpiParams ep;
+  const nvq_status st = epilogue_params("w4a16_gemm_epilogue", epilogue, y_bf16, M, N, &ep);
+  if (st != NVQ_OK) return st;
+  if (spans_meet(bf16_span(x_bf16, M, K, K), bf16_span(y_bf16, M, N, (int64_t)ep.ldy)))
+    return fail(NVQ_ERR_INVALID_ARG, "w4a16_gemm_epilogue: x overlaps y");
+  if (M <= 8) return launch_w4a16<1, false, true>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream, ep);
+  if (M <= 16) return launch_w4a16<2, false, true>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream, ep);
+  return launch_w4a16<4, false, true>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream, ep);
 }
 
 // ------------------------------------------------------------------ 2:4 sparse INT4 decode
@@ -673,6 +778,37 @@ nvq_status nvq_linear(const void* x_bf16, int64_t M, int64_t N, int64_t K, const
   nvq_status st = nvfp4_quantize(x_bf16, M, K, nullptr, xc, xs, tx, ws + L.scratch, L.total - L.scratch, stream);
   if (st != NVQ_OK) return st;
   return nvfp4_gemm_w4a4(xc, xs, tx, w_codes, w_scales, w_t, y_bf16, M, N, K, stream);
+}
+
+nvq_status nvq_linear_epilogue(const void* x_bf16, int64_t M, int64_t N, int64_t K, const uint8_t* w_codes,
+                               const uint8_t* w_scales, const float* w_t, const uint8_t* w_packed_codes,
+                               const void* w_packed_scales, int64_t crossover_m, void* y_bf16,
+                               const nvq_epilogue* epilogue, void* workspace, size_t workspace_bytes, void* stream) {
+  if (crossover_m < 0) crossover_m = kDefaultCrossoverM;
+  if (M <= crossover_m) {
+    if (!w_packed_codes || !w_packed_scales)
+      return fail(NVQ_ERR_INVALID_ARG, "nvq_linear_epilogue: W4A16 path needs the packed INT4 weights");
+    return w4a16_gemm_epilogue(x_bf16, w_packed_codes, w_packed_scales, y_bf16, M, N, K, epilogue, stream);
+  }
+  if (!w_codes || !w_scales || !w_t)
+    return fail(NVQ_ERR_INVALID_ARG, "nvq_linear_epilogue: W4A4 path needs the NVFP4 weights");
+  if (K <= 0 || K % 64 != 0) return fail(NVQ_ERR_UNSUPPORTED_SHAPE, "nvq_linear_epilogue: W4A4 path needs K % 64 == 0");
+  if (N <= 0 || N % 8 != 0) return fail(NVQ_ERR_UNSUPPORTED_SHAPE, "nvq_linear_epilogue: W4A4 path needs N % 8 == 0");
+  const LinearWs L = linear_ws_layout(M, K);
+  if (workspace == nullptr || workspace_bytes < L.total)
+    return fail(NVQ_ERR_WORKSPACE, "nvq_linear_epilogue: workspace too small");
+  if (!aligned16(workspace)) return fail(NVQ_ERR_MISALIGNED, "nvq_linear_epilogue: workspace not 16-byte aligned");
+  if (!y_bf16) return fail(NVQ_ERR_INVALID_ARG, "nvq_linear_epilogue: NULL pointer");
+  nvq::EpiParams ep;                               // the product's own checks, before anything is enqueued
+  nvq_status st = epilogue_params("nvq_linear_epilogue", epilogue, y_bf16, M, N, &ep);
+  if (st != NVQ_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* xc = ws + L.codes;
+  uint8_t* xs = ws + L.scales;
+  float* tx = reinterpret_cast<float*>(ws + L.t);
+  st = nvfp4_quantize(x_bf16, M, K, nullptr, xc, xs, tx, ws + L.scratch, L.total - L.scratch, stream);
+  if (st != NVQ_OK) return st;
+  return nvfp4_gemm_w4a4_epilogue(xc, xs, tx, w_codes, w_scales, w_t, y_bf16, M, N, K, epilogue, stream);
 }
 
 // ------------------------------------------------------------------ prefill with host-resident weights

@@ -41,6 +41,7 @@
 // results are reproducible run to run.
 #pragma once
 #include <cuda_bf16.h>
+#include "epilogue.cuh"
 #include "ptx.cuh"
 
 namespace nvq {
@@ -238,19 +239,41 @@ __device__ __forceinline__ void put_tile(float* p, const float (&a)[NTT][4]) {
 }
 // C fragments of output tile `tn` (16-row MMA tile tt: weight rows ROWS tn + 16 tt + g / + 8;
 // batch columns m0 + 8t + 2c / + 1) -> Y bf16.
-template <int TILES, int NT8>
-__device__ __forceinline__ void store_tile(__nv_bfloat16* __restrict__ y, const float (&acc)[TILES * NT8][4],
-                                           uint32_t tn, uint32_t m0, uint32_t M, uint32_t N, uint32_t lane) {
+// EPI: with bias, activation and residual, and y with a row stride of its own.
+template <int TILES, int NT8, bool EPI>
+__device__ __forceinline__ void store_tile(__nv_bfloat16* y, const float (&acc)[TILES * NT8][4], uint32_t tn,
+                                           uint32_t m0, uint32_t M, uint32_t N, uint32_t lane, const EpiParams& ep) {
+  const size_t ldy = EPI ? ep.ldy : (size_t)N;
 #pragma unroll
   for (int tt = 0; tt < TILES; ++tt) {
     const uint32_t n_lo = (tn * TILES + tt) * 16 + (lane >> 2), n_hi = n_lo + 8;
+    float b_lo = 0.f, b_hi = 0.f;
+    if (EPI && ep.bias != nullptr) {
+      b_lo = __bfloat162float(ep.bias[n_lo]);
+      b_hi = __bfloat162float(ep.bias[n_hi]);
+    }
 #pragma unroll
-    for (int t = 0; t < NT8; ++t)
+    for (int t = 0; t < NT8; ++t) {
+      float v[4] = {acc[tt * NT8 + t][0], acc[tt * NT8 + t][1], acc[tt * NT8 + t][2], acc[tt * NT8 + t][3]};
+      const uint32_t m = m0 + t * 8 + 2 * (lane & 3u);
+      if constexpr (EPI) {
+        float r[4] = {0.f, 0.f, 0.f, 0.f};                  // requested before the activation is computed
+        if (ep.residual != nullptr) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t m = m0 + t * 8 + 2 * (lane & 3u) + (e & 1);
-        if (m < M) y[(size_t)m * N + ((e & 2) ? n_hi : n_lo)] = __float2bfloat16_rn(acc[tt * NT8 + t][e]);
+          for (int e = 0; e < 4; ++e)
+            if (m + (e & 1) < M)
+              r[e] = __bfloat162float(ep.residual[(size_t)(m + (e & 1)) * ep.ldr + ((e & 2) ? n_hi : n_lo)]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += (e & 2) ? b_hi : b_lo;
+        activate(v, ep.act);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += r[e];
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (m + (e & 1) < M) y[(size_t)(m + (e & 1)) * ldy + ((e & 2) ? n_hi : n_lo)] = __float2bfloat16_rn(v[e]);
+    }
   }
 }
 
@@ -378,10 +401,11 @@ __device__ __forceinline__ void sparse_unit(uint32_t unit, uint32_t lane, const 
   }
 }
 
-template <int NT8, bool SPARSE>
+// EPI: bias, activation and residual where a tile is stored (ep; not read otherwise).
+template <int NT8, bool SPARSE, bool EPI>
 __global__ void __launch_bounds__(Cfg<NT8, SPARSE>::THREADS, Cfg<NT8, SPARSE>::MIN_CTAS) w4a16_kernel(
     const __nv_bfloat16* __restrict__ x, const uint8_t* __restrict__ pcodes, const uint8_t* __restrict__ pscales,
-    __nv_bfloat16* __restrict__ y, uint32_t M, uint32_t N, uint32_t K) {
+    __nv_bfloat16* y, uint32_t M, uint32_t N, uint32_t K, const EpiParams ep) {
   using C = Cfg<NT8, SPARSE>;
   using U = typename C::U;
   constexpr uint32_t UC = U::CODE, USC = U::SCALE;
@@ -568,7 +592,7 @@ __global__ void __launch_bounds__(Cfg<NT8, SPARSE>::THREADS, Cfg<NT8, SPARSE>::M
             copy_tile<NTT>(p0, acc);
             has0 = true;
           } else {
-            store_tile<TILES, NT8>(y, acc, nt, m0, M, N, lane);
+            store_tile<TILES, NT8, EPI>(y, acc, nt, m0, M, N, lane, ep);
           }
           zero_tile<NTT>(acc);
           g = 0;
@@ -617,7 +641,7 @@ __global__ void __launch_bounds__(Cfg<NT8, SPARSE>::THREADS, Cfg<NT8, SPARSE>::M
           any |= take;
         }
         if (whole) {
-          if (any) store_tile<TILES, NT8>(y, s, tt, m0, M, N, lane);
+          if (any) store_tile<TILES, NT8, EPI>(y, s, tt, m0, M, N, lane, ep);
         } else if (te > F1) {
           // Rank 0's last tile continues in rank 1: push the partial there.
           if (pass >= 2 && !mbar_wait_cluster(fbar + 8 * par, use ^ 1u)) { ok = false; continue; }
@@ -636,7 +660,7 @@ __global__ void __launch_bounds__(Cfg<NT8, SPARSE>::THREADS, Cfg<NT8, SPARSE>::M
           for (int t = 0; t < NTT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) r[t][e] += s[t][e];
-          store_tile<TILES, NT8>(y, r, tt, m0, M, N, lane);
+          store_tile<TILES, NT8, EPI>(y, r, tt, m0, M, N, lane, ep);
           __syncwarp();                        // every lane has read the slot
           if (lane == 0 && pass + 2 < npass) mbar_arrive_remote(map_to_rank(fbar + 8 * par, 0));
         }
