@@ -420,6 +420,60 @@ nvq_status nvq_linear_epilogue(const void* x_bf16, int64_t M, int64_t N, int64_t
                                void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ *
+ * Mixture-of-experts layer of the decode phase: INT4 experts, a few tokens.
+ *
+ *   logits[t, e] = sum_k x[t, k] w_router[e, k]                       (FP32)
+ *   ids[t, j]    = the expert of the j-th largest logit of t; ties go to the
+ *                  lower index, a NaN counts as larger than any number
+ *   weights[t, j] = exp(l[t, ids[t, j]]) / sum, the sum of exp(l) over the topk
+ *                  chosen experts if renormalize, else over all E (softmax)
+ *   y[t] = residual[t] + sum_j weights[t, j] Wd[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])),
+ *                  e = ids[t, j]
+ *
+ * moe_route computes ids and weights; w4a16_moe_experts y from any ids and
+ * weights; w4a16_moe both (ids and weights are outputs too).
+ *
+ * x_bf16 [T, H], w_router_bf16 [E, H], ids int32 [T, topk], weights FP32
+ * [T, topk], residual_bf16 [T, H] or NULL, y_bf16 [T, H]: row-major, contiguous.
+ * ids of w4a16_moe_experts: a value outside [0, E) is no choice (padded rows: a
+ * token without any choice gets its residual, or 0); an expert that a token
+ * names more than once counts with the sum of those weights.
+ * y may be x or residual (the same pointer); any other overlap of y with them
+ * is NVQ_ERR_INVALID_ARG.
+ * gate_up_codes / gate_up_scales: int4_pack_weights of the stack [E * 2I, H] in
+ * which expert e has rows e * 2I ..., gate and up rows in turn by 16: rows
+ * 32 b .. 32 b + 15 of an expert are gate rows 16 b .. 16 b + 15, the next 16
+ * the same up rows.  down_codes / down_scales: of the stack [E * H, I].
+ * Arithmetic: products as w4a16_gemm; h = weights * silu(gate) * up in FP32,
+ * carried to the down product as the sum of two BF16 numbers (16 bits); the
+ * sum over experts in FP32, one rounding to BF16.  Group and expert sums are
+ * added in an order fixed by the arguments and the GPU's SM count: repeated
+ * calls give identical results.
+ * Any T; experts run 32 tokens per pass over the weights that those tokens
+ * meet (made for T <= 32).
+ * workspace: w4a16_moe_workspace_bytes(T, H, I, topk) device bytes, 16-byte
+ * aligned, of any content; calls that may overlap on the GPU need one each.
+ * Launched with programmatic dependent launch under the rules of w4a16_gemm
+ * (packed weights constant, all else after the wait on the preceding kernel).
+ * Shape rules: T >= 0, 1 <= E <= 512, 1 <= topk <= 16; router: topk <= E,
+ * H % 64 == 0; experts: H % 128 == 0, I % 128 == 0, both < 2^20.  Pointers
+ * 16-byte aligned, ids and weights 4.
+ * ------------------------------------------------------------------------ */
+nvq_status moe_route(const void* x_bf16, const void* w_router_bf16, int64_t T, int64_t E, int64_t H, int topk,
+                     int renormalize, int32_t* ids, float* weights, void* stream);
+size_t w4a16_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int topk);
+nvq_status w4a16_moe_experts(const void* x_bf16, const int32_t* ids, const float* weights,
+                             const uint8_t* gate_up_codes, const void* gate_up_scales,
+                             const uint8_t* down_codes, const void* down_scales, const void* residual_bf16,
+                             void* y_bf16, int64_t T, int64_t E, int64_t H, int64_t I, int topk,
+                             void* workspace, size_t workspace_bytes, void* stream);
+nvq_status w4a16_moe(const void* x_bf16, const void* w_router_bf16, const uint8_t* gate_up_codes,
+                     const void* gate_up_scales, const uint8_t* down_codes, const void* down_scales,
+                     const void* residual_bf16, void* y_bf16, int32_t* ids, float* weights, int64_t T,
+                     int64_t E, int64_t H, int64_t I, int topk, int renormalize, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
  * Prefill over layers whose NVFP4 weights live in pinned host memory
  * (Disaggregated Quantization page, singularity-lens.com, its ODP scheme:
  * prefill weights read layer block by layer block into two device buffers,

@@ -91,6 +91,10 @@ def lib() -> ctypes.CDLL:
             "w4a16_gemm_epilogue": ([vp, vp, vp, vp, i64, i64, i64, ctypes.POINTER(Epilogue), vp], i32),
             "nvq_linear_epilogue": ([vp, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp, ctypes.POINTER(Epilogue), vp, sz,
                                      vp], i32),
+            "moe_route": ([vp, vp, i64, i64, i64, i32, i32, vp, vp, vp], i32),
+            "w4a16_moe_workspace_bytes": ([i64, i64, i64, i32], sz),
+            "w4a16_moe_experts": ([vp] * 9 + [i64, i64, i64, i64, i32, vp, sz, vp], i32),
+            "w4a16_moe": ([vp] * 10 + [i64, i64, i64, i64, i32, i32, vp, sz, vp], i32),
             "int4_quantize": ([vp, i64, i64, vp, vp, vp], i32),
             "int4_pack_weights": ([vp, vp, i64, i64, vp, vp, vp], i32),
             "w4a16_workspace_bytes": ([i64, i64, i64], sz),
@@ -253,12 +257,13 @@ def nvfp4_gemm_w4a4(xq, wq, M: int, N: int, K: int, *, y=None, stream=None):
     return y
 
 
-def interleave_gate_up(w_gate, w_up):
+def interleave_gate_up(w_gate, w_up, block: int = 128):
     """[I, K] gate and up weights -> [2I, K] with rows interleaved in blocks of
-    128 (gate block b, then up block b), the order nvfp4_gemm_w4a4_swiglu reads."""
+    128 (gate block b, then up block b), the order nvfp4_gemm_w4a4_swiglu reads;
+    block = 16 is the order of the experts of w4a16_moe."""
     I, K = w_gate.shape
-    assert w_up.shape == (I, K) and I % 128 == 0
-    return torch.stack([w_gate.view(I // 128, 128, K), w_up.view(I // 128, 128, K)], dim=1).reshape(2 * I, K)
+    assert w_up.shape == (I, K) and I % block == 0
+    return torch.stack([w_gate.view(I // block, block, K), w_up.view(I // block, block, K)], dim=1).reshape(2 * I, K)
 
 
 def nvfp4_gemm_w4a4_swiglu(xq, wq, M: int, N: int, K: int, t_h, *, h_codes=None, h_scales=None, stream=None):
@@ -514,6 +519,98 @@ def nvq_linear_epilogue(x, w4a4=None, w4a16=None, N: int | None = None, *, bias=
         _check(lib().nvq_linear_epilogue(x.data_ptr(), M, N, K, *w, crossover_m, y.data_ptr(), ctypes.byref(e),
                                          _ptr(workspace), ws_bytes, _stream(stream)), "nvq_linear_epilogue")
     return y
+
+
+# ------------------------------------------------------------------ mixture of experts
+def w4a16_moe_workspace_bytes(T: int, H: int, I: int, topk: int) -> int:
+    return int(lib().w4a16_moe_workspace_bytes(T, H, I, topk))
+
+
+def _tokens(x):
+    dev = _cuda_device(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    _need(x, "x", dev, torch.bfloat16)
+    return dev, *x.shape
+
+
+def _choices(dev, T, topk, ids, weights):
+    if ids is None:
+        ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty(T, topk, dtype=torch.float32, device=dev)
+    _need(ids, "ids", dev, torch.int32, shape=(T, topk))
+    _need(weights, "weights", dev, torch.float32, shape=(T, topk))
+    return ids, weights
+
+
+def _expert_tensors(dev, T, E, H, I, topk, gate_up, down, residual, y, workspace):
+    """Checks the experts' arguments and allocates what the caller left out."""
+    for (c, s), name, n in ((gate_up, "gate_up", 2 * I * H), (down, "down", H * I)):
+        _need(c, name + " codes", dev, torch.uint8, numel=E * n // 2)
+        _need(s, name + " scales", dev, torch.uint8, numel=E * n // 64)
+    if residual is not None:
+        _need(residual, "residual", dev, torch.bfloat16, shape=(T, H))
+    if y is None:
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    _need(y, "y", dev, torch.bfloat16, shape=(T, H))
+    if workspace is None:
+        workspace = torch.empty(w4a16_moe_workspace_bytes(T, H, I, topk), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", dev, workspace.dtype)
+    return y, workspace, workspace.numel() * workspace.element_size()
+
+
+def moe_route(x, w_router, topk: int, *, renormalize: bool = True, ids=None, weights=None, stream=None):
+    """The topk experts of each token and their weights: (ids int32 [T, topk], weights float32 [T, topk]).
+
+    x [T, H] bf16, w_router [E, H] bf16; softmax over the chosen experts, or
+    over all E with renormalize=False."""
+    dev, T, H = _tokens(x)
+    E = w_router.shape[0]
+    _need(w_router, "w_router", dev, torch.bfloat16, shape=(E, H))
+    with _on(dev, stream):
+        ids, weights = _choices(dev, T, topk, ids, weights)
+        _check(lib().moe_route(x.data_ptr(), w_router.data_ptr(), T, E, H, topk, int(renormalize), ids.data_ptr(),
+                               weights.data_ptr(), _stream(stream)), "moe_route")
+    return ids, weights
+
+
+def w4a16_moe_experts(x, ids, weights, gate_up, down, E: int, I: int, *, residual=None, y=None, workspace=None,
+                      stream=None):
+    """Y [T, H] bf16 = residual + sum over a token's choices of weight * down(silu(gate x) * (up x)).
+
+    ids int32 / weights float32 [T, topk] (an id outside [0, E) is no choice);
+    gate_up, down: (packed_codes, packed_scales) of int4_pack_weights over the
+    stacked experts, [E * 2I, H] (each expert interleave_gate_up(..., block=16))
+    and [E * H, I].  y may be x or residual."""
+    dev, T, H = _tokens(x)
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, topk]")
+    topk = ids.shape[1]
+    with _on(dev, stream):
+        _choices(dev, T, topk, ids, weights)
+        y, workspace, ws_bytes = _expert_tensors(dev, T, E, H, I, topk, gate_up, down, residual, y, workspace)
+        _check(lib().w4a16_moe_experts(x.data_ptr(), ids.data_ptr(), weights.data_ptr(), gate_up[0].data_ptr(),
+                                       gate_up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), _ptr(residual),
+                                       y.data_ptr(), T, E, H, I, topk, workspace.data_ptr(), ws_bytes,
+                                       _stream(stream)), "w4a16_moe_experts")
+    return y
+
+
+def w4a16_moe(x, w_router, gate_up, down, I: int, topk: int, *, renormalize: bool = True, residual=None, ids=None,
+              weights=None, y=None, workspace=None, stream=None):
+    """The whole layer: moe_route, then w4a16_moe_experts.  Returns (y, ids, weights)."""
+    dev, T, H = _tokens(x)
+    E = w_router.shape[0]
+    _need(w_router, "w_router", dev, torch.bfloat16, shape=(E, H))
+    with _on(dev, stream):
+        ids, weights = _choices(dev, T, topk, ids, weights)
+        y, workspace, ws_bytes = _expert_tensors(dev, T, E, H, I, topk, gate_up, down, residual, y, workspace)
+        _check(lib().w4a16_moe(x.data_ptr(), w_router.data_ptr(), gate_up[0].data_ptr(), gate_up[1].data_ptr(),
+                               down[0].data_ptr(), down[1].data_ptr(), _ptr(residual), y.data_ptr(), ids.data_ptr(),
+                               weights.data_ptr(), T, E, H, I, topk, int(renormalize), workspace.data_ptr(), ws_bytes,
+                               _stream(stream)), "w4a16_moe")
+    return y, ids, weights
 
 
 def _stream_layers(layers):

@@ -13,6 +13,7 @@
 
 #include "../../include/nvq.h"
 #include "int4.cuh"
+#include "moe.cuh"
 #include "nvfp4_gemm.cuh"
 #include "nvfp4_quantize.cuh"
 #include "ptx.cuh"
@@ -729,6 +730,218 @@ nvq_status w4a16_sparse24_gemm(const void* x_bf16, const uint8_t* packed, const 
   if (M <= 8) return launch_w4a16<1, true>(x_bf16, packed, packed_scales, y_bf16, M, N, K, stream);
   if (M <= 16) return launch_w4a16<2, true>(x_bf16, packed, packed_scales, y_bf16, M, N, K, stream);
   return launch_w4a16<4, true>(x_bf16, packed, packed_scales, y_bf16, M, N, K, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ mixture of experts
+namespace {
+
+// CTAs of the expert kernels: two on each of a B200's SMs.  A constant, so that
+// the workspace (one partial tile pair per CTA of the down kernel) can be sized without a device.
+constexpr int kMoeMaxGrid = 2 * 148;
+constexpr int64_t kMoeMaxDim = (int64_t)1 << 20;   // H and I: a CTA's unit counts stay in 32 bits
+
+struct MoeWs {
+  size_t hi, lo, tickets, partial, total;
+};
+MoeWs moe_ws_layout(int64_t T, int64_t H, int64_t I, int64_t topk) {
+  const size_t tc = (size_t)std::min<int64_t>(T, nvq::moe::kMaxTokens);
+  const size_t half = align256(tc * (size_t)topk * (size_t)I * 2);
+  MoeWs W;
+  W.hi = 0;
+  W.lo = half;
+  W.tickets = 2 * half;
+  W.partial = W.tickets + align256((size_t)(H / 32) * 4);
+  W.total = W.partial + (size_t)2 * kMoeMaxGrid * tc * 32 * 4;
+  return W;
+}
+
+// Once per device and kernel: the shared-memory opt-in.
+template <typename K>
+nvq_status smem_opt_in(K kernel, int bytes, std::once_flag (&once)[kMaxDevices], cudaError_t (&err)[kMaxDevices],
+                       const char* where) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  if (dev < 0 || dev >= kMaxDevices) return fail(NVQ_ERR_CUDA, "device index out of range");
+  std::call_once(once[dev], [&] { err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+  return err[dev] == cudaSuccess ? NVQ_OK : cuda_fail(err[dev], where);
+}
+
+// A launch that may begin during the preceding kernel's tail; `cluster` CTAs per cluster (0: none).
+template <typename... P, typename... A>
+nvq_status launch_dependent(const char* where, void (*kernel)(P...), int grid, int threads, size_t smem, int cluster,
+                            cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  return launch_status(where);
+}
+
+nvq_status route_validate(const char* name, const void* x, const void* wr, int64_t T, int64_t E, int64_t H, int topk,
+                          const int32_t* ids, const float* weights) {
+  char msg[160];
+  auto bad = [&](nvq_status s, const char* what) {
+    snprintf(msg, sizeof(msg), "%s: %s", name, what);
+    return fail(s, msg);
+  };
+  if (T < 0 || E <= 0 || H <= 0 || topk <= 0) return bad(NVQ_ERR_INVALID_ARG, "bad sizes");
+  if (topk > E) return bad(NVQ_ERR_INVALID_ARG, "topk > E");
+  if (E > nvq::moe::kMaxExperts || topk > nvq::moe::kMaxTopk) return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "need E <= 512, topk <= 16");
+  if (H % 64 != 0 || H >= kMaxDim) return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "need H % 64 == 0, H < 2^31");
+  if (T >= kMaxDim) return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "too many tokens");
+  if (T > 0 && (!x || !wr || !ids || !weights)) return bad(NVQ_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned16(x) || !aligned16(wr) || (reinterpret_cast<uintptr_t>(ids) & 3u) || (reinterpret_cast<uintptr_t>(weights) & 3u))
+    return bad(NVQ_ERR_MISALIGNED, "x or w_router not 16-byte, ids or weights not 4-byte aligned");
+  return NVQ_OK;
+}
+
+nvq_status experts_validate(const char* name, const void* x, const int32_t* ids, const float* weights,
+                            const void* const (&packed)[4], const void* residual, const void* y, int64_t T, int64_t E,
+                            int64_t H, int64_t I, int topk, const void* workspace, size_t workspace_bytes) {
+  char msg[160];
+  auto bad = [&](nvq_status s, const char* what) {
+    snprintf(msg, sizeof(msg), "%s: %s", name, what);
+    return fail(s, msg);
+  };
+  if (T < 0 || E <= 0 || H <= 0 || I <= 0 || topk <= 0) return bad(NVQ_ERR_INVALID_ARG, "bad sizes");
+  if (E > nvq::moe::kMaxExperts || topk > nvq::moe::kMaxTopk) return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "need E <= 512, topk <= 16");
+  if (H % 128 != 0 || I % 128 != 0 || H >= kMoeMaxDim || I >= kMoeMaxDim)
+    return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "need H % 128 == 0, I % 128 == 0, both < 2^20");
+  if (T >= kMaxDim) return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "too many tokens");
+  if (T == 0) return NVQ_OK;
+  if (!x || !ids || !weights || !y) return bad(NVQ_ERR_INVALID_ARG, "NULL pointer");
+  for (const void* q : packed)
+    if (!q) return bad(NVQ_ERR_INVALID_ARG, "NULL weights");
+  for (const void* q : packed)
+    if (!aligned16(q)) return bad(NVQ_ERR_MISALIGNED, "packed weights not 16-byte aligned");
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(y) || (reinterpret_cast<uintptr_t>(ids) & 3u) ||
+      (reinterpret_cast<uintptr_t>(weights) & 3u))
+    return bad(NVQ_ERR_MISALIGNED, "x, residual or y not 16-byte, ids or weights not 4-byte aligned");
+  if (!may_alias_y(x, H, y, H, T, H)) return bad(NVQ_ERR_INVALID_ARG, "x overlaps y without being y");
+  if (residual && !may_alias_y(residual, H, y, H, T, H)) return bad(NVQ_ERR_INVALID_ARG, "residual overlaps y without being y");
+  if (!workspace || workspace_bytes < moe_ws_layout(T, H, I, topk).total) return bad(NVQ_ERR_WORKSPACE, "workspace missing or too small");
+  if (!aligned16(workspace)) return bad(NVQ_ERR_MISALIGNED, "workspace not 16-byte aligned");
+  return NVQ_OK;
+}
+
+nvq_status launch_route(const void* x, const void* wr, int64_t T, int64_t E, int64_t H, int topk, bool renorm,
+                        int32_t* ids, float* weights, cudaStream_t stream) {
+  using namespace nvq::moe;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t err[kMaxDevices];
+  const nvq_status st = smem_opt_in(route_kernel, RouteShape(kMaxExperts).smem(), once, err, "moe_route: smem attribute");
+  if (st != NVQ_OK) return st;
+  const int64_t clusters = (T + kMaxTokens - 1) / kMaxTokens;
+  return launch_dependent("route_kernel", route_kernel, (int)(clusters * RCS), RTHREADS, RouteShape((int)E).smem(), RCS,
+                          stream, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(wr),
+                          (uint32_t)T, (uint32_t)E, (uint32_t)H, (uint32_t)topk, renorm ? 1u : 0u, ids, weights);
+}
+
+// 32 tokens at a time: gate and up, then down.
+nvq_status launch_experts(nvq::moe::ExpertParams p, int64_t T, void* workspace, cudaStream_t stream) {
+  using namespace nvq::moe;
+  const MoeWs W = moe_ws_layout(T, p.H, p.I, p.topk);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.h_hi = reinterpret_cast<__nv_bfloat16*>(ws + W.hi);
+  p.h_lo = reinterpret_cast<__nv_bfloat16*>(ws + W.lo);
+  p.tickets = reinterpret_cast<uint32_t*>(ws + W.tickets);
+  p.partial = reinterpret_cast<float*>(ws + W.partial);
+  const int grid = std::min(kMoeMaxGrid, 2 * sm_count());
+  for (int64_t t0 = 0; t0 < T; t0 += kMaxTokens) {
+    p.T = (uint32_t)std::min<int64_t>(kMaxTokens, T - t0);
+    nvq_status st = launch_dependent("gate_up_kernel", gate_up_kernel, grid, ETHREADS, 0, 0, stream, p);
+    if (st == NVQ_OK)
+      st = launch_dependent("down_kernel", down_kernel, grid, ETHREADS, (size_t)EWARPS * p.T * 32 * 4, 0, stream, p);
+    if (st != NVQ_OK) return st;
+    p.x += (size_t)p.T * p.H;
+    p.y += (size_t)p.T * p.H;
+    if (p.residual) p.residual += (size_t)p.T * p.H;
+    p.ids += (size_t)p.T * p.topk;
+    p.weights += (size_t)p.T * p.topk;
+  }
+  return NVQ_OK;
+}
+
+nvq::moe::ExpertParams expert_params(const void* x, const int32_t* ids, const float* weights,
+                                     const void* const (&packed)[4], const void* residual, void* y, int64_t E,
+                                     int64_t H, int64_t I, int topk) {
+  nvq::moe::ExpertParams p = {};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.ids = ids;
+  p.weights = weights;
+  p.gu_codes = static_cast<const uint8_t*>(packed[0]);
+  p.gu_scales = static_cast<const uint8_t*>(packed[1]);
+  p.d_codes = static_cast<const uint8_t*>(packed[2]);
+  p.d_scales = static_cast<const uint8_t*>(packed[3]);
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.E = (uint32_t)E;
+  p.H = (uint32_t)H;
+  p.I = (uint32_t)I;
+  p.topk = (uint32_t)topk;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+nvq_status moe_route(const void* x_bf16, const void* w_router_bf16, int64_t T, int64_t E, int64_t H, int topk,
+                     int renormalize, int32_t* ids, float* weights, void* stream) {
+  const nvq_status st = route_validate("moe_route", x_bf16, w_router_bf16, T, E, H, topk, ids, weights);
+  if (st != NVQ_OK || T == 0) return st;
+  return launch_route(x_bf16, w_router_bf16, T, E, H, topk, renormalize != 0, ids, weights,
+                      static_cast<cudaStream_t>(stream));
+}
+
+size_t w4a16_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int topk) {
+  if (T <= 0 || H <= 0 || I <= 0 || topk <= 0 || H >= kMoeMaxDim || I >= kMoeMaxDim || topk > nvq::moe::kMaxTopk) return 0;
+  return moe_ws_layout(T, H, I, topk).total;
+}
+
+nvq_status w4a16_moe_experts(const void* x_bf16, const int32_t* ids, const float* weights,
+                             const uint8_t* gate_up_codes, const void* gate_up_scales, const uint8_t* down_codes,
+                             const void* down_scales, const void* residual_bf16, void* y_bf16, int64_t T, int64_t E,
+                             int64_t H, int64_t I, int topk, void* workspace, size_t workspace_bytes, void* stream) {
+  const void* const packed[4] = {gate_up_codes, gate_up_scales, down_codes, down_scales};
+  const nvq_status st = experts_validate("w4a16_moe_experts", x_bf16, ids, weights, packed, residual_bf16, y_bf16, T, E,
+                                         H, I, topk, workspace, workspace_bytes);
+  if (st != NVQ_OK || T == 0) return st;
+  return launch_experts(expert_params(x_bf16, ids, weights, packed, residual_bf16, y_bf16, E, H, I, topk), T, workspace,
+                        static_cast<cudaStream_t>(stream));
+}
+
+nvq_status w4a16_moe(const void* x_bf16, const void* w_router_bf16, const uint8_t* gate_up_codes,
+                     const void* gate_up_scales, const uint8_t* down_codes, const void* down_scales,
+                     const void* residual_bf16, void* y_bf16, int32_t* ids, float* weights, int64_t T, int64_t E,
+                     int64_t H, int64_t I, int topk, int renormalize, void* workspace, size_t workspace_bytes,
+                     void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const void* const packed[4] = {gate_up_codes, gate_up_scales, down_codes, down_scales};
+  nvq_status st = route_validate("w4a16_moe", x_bf16, w_router_bf16, T, E, H, topk, ids, weights);
+  if (st != NVQ_OK) return st;
+  st = experts_validate("w4a16_moe", x_bf16, ids, weights, packed, residual_bf16, y_bf16, T, E, H, I, topk, workspace,
+                        workspace_bytes);
+  if (st != NVQ_OK || T == 0) return st;
+  st = launch_route(x_bf16, w_router_bf16, T, E, H, topk, renormalize != 0, ids, weights, stream);
+  if (st != NVQ_OK) return st;
+  return launch_experts(expert_params(x_bf16, ids, weights, packed, residual_bf16, y_bf16, E, H, I, topk), T, workspace,
+                        stream);
 }
 
 // ------------------------------------------------------------------ phase dispatch
