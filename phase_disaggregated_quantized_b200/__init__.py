@@ -16,8 +16,8 @@ ending in ``_epilogue`` add bias, activation and residual to those products.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import re
 
@@ -386,56 +386,66 @@ def nvq_linear(x, w4a4=None, w4a16=None, N: int | None = None, *, crossover_m: i
 
 
 # ------------------------------------------------------------------ products with an epilogue
-def _on(dev, stream):
-    """The context of one call on tensors of `dev`: that device current and, when the
-    caller names a stream, what the call allocates belonging to that stream."""
+# These calls are a few microseconds on the GPU, so the binding looks at each
+# tensor once and takes the stream's handle without making a stream object.
+def _elsewhere(idx, stream):
+    """None if a call on tensors of device idx can be made as things are: the device is current and
+    no stream is named.  Else the context to make it in (what it allocates then belongs to that stream)."""
     if stream is None:
-        return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        return None if idx == torch.cuda.current_device() else torch.cuda.device(idx)
+    if stream.device.index != idx:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{idx}")
     return torch.cuda.stream(stream)
 
 
-def _need(t, name, dev, dtype, shape=None, numel=None):
-    """A contiguous tensor of this type and size on the call's device."""
-    if t.device != dev or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {dev}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if numel is not None and t.numel() * t.element_size() < numel:
-        raise ValueError(f"{name} must hold at least {numel} bytes")
-
-
-def _need_rows(t, name, dev, M, N):
-    """A BF16 [M, N] tensor with contiguous rows; returns its row stride (0: N)."""
-    if t.device != dev or t.dtype != torch.bfloat16 or t.dim() != 2 or t.shape[0] != M or t.shape[1] != N:
-        raise ValueError(f"{name} must be a [{M}, {N}] bfloat16 tensor on {dev}")
-    if M <= 1 and (N <= 1 or t.stride(1) == 1):
-        return 0
-    if t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0)
-
-
-def _cuda_device(x, name):
-    if not x.is_cuda:
+def _device_of(t, name):
+    idx = t.get_device() if t.is_cuda else -1
+    if idx < 0:
         raise ValueError(f"libnvq calls take CUDA tensors ({name})")
-    return x.device
+    return idx
 
 
-def _epilogue(dev, M, N, bias, activation, residual, y):
-    if activation not in ACTIVATIONS:
+def _handle(idx):
+    """The current stream of device idx as a cudaStream_t."""
+    return torch._C._cuda_getCurrentRawStream(idx)
+
+
+def _need(t, name, idx, dtype, nbytes=0):
+    """The address of a contiguous tensor of this type and at least this size on the call's device."""
+    if t.dtype is not dtype or not t.is_cuda or t.get_device() != idx or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{idx}")
+    if t.nbytes < nbytes:
+        raise ValueError(f"{name} must hold at least {nbytes} bytes")
+    return t.data_ptr()
+
+
+def _need_shape(t, name, idx, dtype, shape):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    return _need(t, name, idx, dtype)
+
+
+def _need_rows(t, name, idx, M, N):
+    """Address and row stride (0: N) of a BF16 [M, N] tensor with contiguous rows."""
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.get_device() != idx or t.shape != (M, N):
+        raise ValueError(f"{name} must be a [{M}, {N}] bfloat16 tensor on cuda:{idx}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    ld, step = t.stride()
+    if step != 1 and N > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), ld if M > 1 else 0
+
+
+def _epilogue(idx, M, N, bias, activation, residual, y):
+    """(address of y, nvq_epilogue)."""
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
-    e = Epilogue()
-    if bias is not None:
-        _need(bias, "bias", dev, torch.bfloat16, shape=(N,))
-        e.bias_bf16 = bias.data_ptr()
-    if residual is not None:
-        e.residual_stride = _need_rows(residual, "residual", dev, M, N)
-        e.residual_bf16 = residual.data_ptr()
-    e.y_stride = _need_rows(y, "y", dev, M, N)
-    e.activation = ACTIVATIONS[activation]
-    return e
+    b = None if bias is None else _need_shape(bias, "bias", idx, torch.bfloat16, (N,))
+    r, ldr = (None, 0) if residual is None else _need_rows(residual, "residual", idx, M, N)
+    yp, ldy = _need_rows(y, "y", idx, M, N)
+    return yp, Epilogue(b, r, ldr, ldy, act)
 
 
 def nvfp4_gemm_w4a4_epilogue(xq, wq, M: int, N: int, K: int, *, bias=None, activation: str = "none", residual=None,
@@ -446,20 +456,21 @@ def nvfp4_gemm_w4a4_epilogue(xq, wq, M: int, N: int, K: int, *, bias=None, activ
     a name of ACTIVATIONS; residual: [M, N] bf16.  residual and y may be views
     with contiguous rows (a row stride that is a multiple of 8), and residual
     may be y: the residual stream updated in place."""
-    xc, xs, tx = xq
-    wc, ws, tw = wq
-    dev = _cuda_device(xc, "xq")
+    idx = _device_of(xq[0], "xq")
+    away = _elsewhere(idx, stream)
+    if away is not None:
+        with away:
+            return nvfp4_gemm_w4a4_epilogue(xq, wq, M, N, K, bias=bias, activation=activation, residual=residual, y=y)
+    ptrs = []
     for name, (c, s, t), rows in (("xq", xq, M), ("wq", wq, N)):
-        _need(c, name + " codes", dev, torch.uint8, numel=rows * (K // 2))
-        _need(s, name + " scales", dev, torch.uint8, numel=nvfp4_scales_bytes(rows, K))
-        _need(t, name + " t", dev, torch.float32, numel=4)
-    with _on(dev, stream):
-        if y is None:
-            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-        e = _epilogue(dev, M, N, bias, activation, residual, y)
-        _check(lib().nvfp4_gemm_w4a4_epilogue(xc.data_ptr(), xs.data_ptr(), tx.data_ptr(), wc.data_ptr(),
-                                              ws.data_ptr(), tw.data_ptr(), y.data_ptr(), M, N, K, ctypes.byref(e),
-                                              _stream(stream)), "nvfp4_gemm_w4a4_epilogue")
+        ptrs += (_need(c, name + " codes", idx, torch.uint8, rows * (K // 2)),
+                 _need(s, name + " scales", idx, torch.uint8, (rows + 127) // 128 * 128 * (K // 16)),
+                 _need(t, name + " t", idx, torch.float32, 4))
+    if y is None:
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=xq[0].device)
+    yp, e = _epilogue(idx, M, N, bias, activation, residual, y)
+    _check(lib().nvfp4_gemm_w4a4_epilogue(*ptrs, yp, M, N, K, ctypes.byref(e), _handle(idx)),
+           "nvfp4_gemm_w4a4_epilogue")
     return y
 
 
@@ -468,96 +479,102 @@ def w4a16_gemm_epilogue(x, packed_codes, packed_scales, N: int, *, bias=None, ac
     """Y [M, N] bf16 = act(X W^T + bias) + residual for packed INT4 W [N, K]
     (int4_pack_weights).  bias, activation, residual, y as in
     nvfp4_gemm_w4a4_epilogue; x may not overlap y."""
-    dev = _cuda_device(x, "x")
+    idx = _device_of(x, "x")
+    away = _elsewhere(idx, stream)
+    if away is not None:
+        with away:
+            return w4a16_gemm_epilogue(x, packed_codes, packed_scales, N, bias=bias, activation=activation,
+                                       residual=residual, y=y)
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
-    _need(x, "x", dev, torch.bfloat16)
-    _need(packed_codes, "packed_codes", dev, torch.uint8, numel=N * K // 2)
-    _need(packed_scales, "packed_scales", dev, torch.uint8, numel=N * (K // 128) * 2)
-    with _on(dev, stream):
-        if y is None:
-            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-        e = _epilogue(dev, M, N, bias, activation, residual, y)
-        _check(lib().w4a16_gemm_epilogue(x.data_ptr(), packed_codes.data_ptr(), packed_scales.data_ptr(),
-                                         y.data_ptr(), M, N, K, ctypes.byref(e), _stream(stream)),
-               "w4a16_gemm_epilogue")
+    xp = _need(x, "x", idx, torch.bfloat16)
+    pc = _need(packed_codes, "packed_codes", idx, torch.uint8, N * K // 2)
+    ps = _need(packed_scales, "packed_scales", idx, torch.uint8, N * (K // 128) * 2)
+    if y is None:
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+    yp, e = _epilogue(idx, M, N, bias, activation, residual, y)
+    _check(lib().w4a16_gemm_epilogue(xp, pc, ps, yp, M, N, K, ctypes.byref(e), _handle(idx)), "w4a16_gemm_epilogue")
     return y
 
 
 def nvq_linear_epilogue(x, w4a4=None, w4a16=None, N: int | None = None, *, bias=None, activation: str = "none",
                         residual=None, crossover_m: int = -1, y=None, workspace=None, stream=None):
     """nvq_linear with bias, activation and residual in the product it picks."""
-    dev = _cuda_device(x, "x")
+    idx = _device_of(x, "x")
+    away = _elsewhere(idx, stream)
+    if away is not None:
+        with away:
+            return nvq_linear_epilogue(x, w4a4, w4a16, N, bias=bias, activation=activation, residual=residual,
+                                       crossover_m=crossover_m, y=y, workspace=workspace)
     if N is None:
         raise ValueError("N is required")
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
-    _need(x, "x", dev, torch.bfloat16)
+    xp = _need(x, "x", idx, torch.bfloat16)
     w = [None] * 5
     if w4a4 is not None:
-        for t, name, dt, n in zip(w4a4, ("codes", "scales", "t"), (torch.uint8, torch.uint8, torch.float32),
-                                  (N * (K // 2), nvfp4_scales_bytes(N, K), 4)):
-            _need(t, "w4a4 " + name, dev, dt, numel=n)
-        w[:3] = (t.data_ptr() for t in w4a4)
+        c, s, t = w4a4
+        w[:3] = (_need(c, "w4a4 codes", idx, torch.uint8, N * (K // 2)),
+                 _need(s, "w4a4 scales", idx, torch.uint8, (N + 127) // 128 * 128 * (K // 16)),
+                 _need(t, "w4a4 t", idx, torch.float32, 4))
     if w4a16 is not None:
-        for t, name, n in zip(w4a16, ("codes", "scales"), (N * K // 2, N * (K // 128) * 2)):
-            _need(t, "w4a16 " + name, dev, torch.uint8, numel=n)
-        w[3:] = (t.data_ptr() for t in w4a16)
-    with _on(dev, stream):
-        if y is None:
-            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-        need = nvq_linear_workspace_bytes(M, N, K, crossover_m)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws_bytes = 0
-        if workspace is not None:
-            _need(workspace, "workspace", dev, workspace.dtype)
-            ws_bytes = workspace.numel() * workspace.element_size()
-        e = _epilogue(dev, M, N, bias, activation, residual, y)
-        _check(lib().nvq_linear_epilogue(x.data_ptr(), M, N, K, *w, crossover_m, y.data_ptr(), ctypes.byref(e),
-                                         _ptr(workspace), ws_bytes, _stream(stream)), "nvq_linear_epilogue")
+        c, s = w4a16
+        w[3:] = (_need(c, "w4a16 codes", idx, torch.uint8, N * K // 2),
+                 _need(s, "w4a16 scales", idx, torch.uint8, N * (K // 128) * 2))
+    if y is None:
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+    need = nvq_linear_workspace_bytes(M, N, K, crossover_m)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    wp, wn = (None, 0) if workspace is None else (_need(workspace, "workspace", idx, workspace.dtype), workspace.nbytes)
+    yp, e = _epilogue(idx, M, N, bias, activation, residual, y)
+    _check(lib().nvq_linear_epilogue(xp, M, N, K, *w, crossover_m, yp, ctypes.byref(e), wp, wn, _handle(idx)),
+           "nvq_linear_epilogue")
     return y
 
 
 # ------------------------------------------------------------------ mixture of experts
+@functools.lru_cache(maxsize=256)
 def w4a16_moe_workspace_bytes(T: int, H: int, I: int, topk: int) -> int:
     return int(lib().w4a16_moe_workspace_bytes(T, H, I, topk))
 
 
-def _tokens(x):
-    dev = _cuda_device(x, "x")
+def _tokens(x, idx):
+    """(address, T, H) of the layer's input."""
     if x.dim() != 2:
         raise ValueError("x must be [T, H]")
-    _need(x, "x", dev, torch.bfloat16)
-    return dev, *x.shape
+    T, H = x.shape
+    return _need(x, "x", idx, torch.bfloat16), T, H
 
 
-def _choices(dev, T, topk, ids, weights):
+def _choices(x, idx, T, topk, ids, weights):
     if ids is None:
-        ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
+        ids = torch.empty(T, topk, dtype=torch.int32, device=x.device)
     if weights is None:
-        weights = torch.empty(T, topk, dtype=torch.float32, device=dev)
-    _need(ids, "ids", dev, torch.int32, shape=(T, topk))
-    _need(weights, "weights", dev, torch.float32, shape=(T, topk))
-    return ids, weights
+        weights = torch.empty(T, topk, dtype=torch.float32, device=x.device)
+    shape = (T, topk)
+    return (ids, weights, _need_shape(ids, "ids", idx, torch.int32, shape),
+            _need_shape(weights, "weights", idx, torch.float32, shape))
 
 
-def _expert_tensors(dev, T, E, H, I, topk, gate_up, down, residual, y, workspace):
-    """Checks the experts' arguments and allocates what the caller left out."""
-    for (c, s), name, n in ((gate_up, "gate_up", 2 * I * H), (down, "down", H * I)):
-        _need(c, name + " codes", dev, torch.uint8, numel=E * n // 2)
-        _need(s, name + " scales", dev, torch.uint8, numel=E * n // 64)
-    if residual is not None:
-        _need(residual, "residual", dev, torch.bfloat16, shape=(T, H))
+def _experts(x, idx, T, E, H, I, topk, gate_up, down, residual, y, workspace):
+    """Checks the experts' arguments and allocates what the caller left out: (y, workspace, addresses of
+    the four packed tensors, residual and y, address and size of the workspace)."""
+    gc, gs = gate_up
+    dc, ds = down
+    n = E * I * H
+    ptrs = (_need(gc, "gate_up codes", idx, torch.uint8, n), _need(gs, "gate_up scales", idx, torch.uint8, n // 32),
+            _need(dc, "down codes", idx, torch.uint8, n // 2), _need(ds, "down scales", idx, torch.uint8, n // 64))
+    shape = (T, H)
+    r = None if residual is None else _need_shape(residual, "residual", idx, torch.bfloat16, shape)
     if y is None:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
-    _need(y, "y", dev, torch.bfloat16, shape=(T, H))
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+    yp = _need_shape(y, "y", idx, torch.bfloat16, shape)
     if workspace is None:
-        workspace = torch.empty(w4a16_moe_workspace_bytes(T, H, I, topk), dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", dev, workspace.dtype)
-    return y, workspace, workspace.numel() * workspace.element_size()
+        workspace = torch.empty(w4a16_moe_workspace_bytes(T, H, I, topk), dtype=torch.uint8, device=x.device)
+    return y, workspace, (*ptrs, r, yp), (_need(workspace, "workspace", idx, workspace.dtype), workspace.nbytes)
 
 
 def moe_route(x, w_router, topk: int, *, renormalize: bool = True, ids=None, weights=None, stream=None):
@@ -565,13 +582,16 @@ def moe_route(x, w_router, topk: int, *, renormalize: bool = True, ids=None, wei
 
     x [T, H] bf16, w_router [E, H] bf16; softmax over the chosen experts, or
     over all E with renormalize=False."""
-    dev, T, H = _tokens(x)
+    idx = _device_of(x, "x")
+    away = _elsewhere(idx, stream)
+    if away is not None:
+        with away:
+            return moe_route(x, w_router, topk, renormalize=renormalize, ids=ids, weights=weights)
+    xp, T, H = _tokens(x, idx)
     E = w_router.shape[0]
-    _need(w_router, "w_router", dev, torch.bfloat16, shape=(E, H))
-    with _on(dev, stream):
-        ids, weights = _choices(dev, T, topk, ids, weights)
-        _check(lib().moe_route(x.data_ptr(), w_router.data_ptr(), T, E, H, topk, int(renormalize), ids.data_ptr(),
-                               weights.data_ptr(), _stream(stream)), "moe_route")
+    rp = _need_shape(w_router, "w_router", idx, torch.bfloat16, (E, H))
+    ids, weights, ip, wp = _choices(x, idx, T, topk, ids, weights)
+    _check(lib().moe_route(xp, rp, T, E, H, topk, 1 if renormalize else 0, ip, wp, _handle(idx)), "moe_route")
     return ids, weights
 
 
@@ -583,33 +603,37 @@ def w4a16_moe_experts(x, ids, weights, gate_up, down, E: int, I: int, *, residua
     gate_up, down: (packed_codes, packed_scales) of int4_pack_weights over the
     stacked experts, [E * 2I, H] (each expert interleave_gate_up(..., block=16))
     and [E * H, I].  y may be x or residual."""
-    dev, T, H = _tokens(x)
+    idx = _device_of(x, "x")
+    away = _elsewhere(idx, stream)
+    if away is not None:
+        with away:
+            return w4a16_moe_experts(x, ids, weights, gate_up, down, E, I, residual=residual, y=y, workspace=workspace)
+    xp, T, H = _tokens(x, idx)
     if ids.dim() != 2:
         raise ValueError("ids must be [T, topk]")
     topk = ids.shape[1]
-    with _on(dev, stream):
-        _choices(dev, T, topk, ids, weights)
-        y, workspace, ws_bytes = _expert_tensors(dev, T, E, H, I, topk, gate_up, down, residual, y, workspace)
-        _check(lib().w4a16_moe_experts(x.data_ptr(), ids.data_ptr(), weights.data_ptr(), gate_up[0].data_ptr(),
-                                       gate_up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), _ptr(residual),
-                                       y.data_ptr(), T, E, H, I, topk, workspace.data_ptr(), ws_bytes,
-                                       _stream(stream)), "w4a16_moe_experts")
+    _, _, ip, wp = _choices(x, idx, T, topk, ids, weights)
+    y, workspace, ptrs, ws = _experts(x, idx, T, E, H, I, topk, gate_up, down, residual, y, workspace)
+    _check(lib().w4a16_moe_experts(xp, ip, wp, *ptrs, T, E, H, I, topk, *ws, _handle(idx)), "w4a16_moe_experts")
     return y
 
 
 def w4a16_moe(x, w_router, gate_up, down, I: int, topk: int, *, renormalize: bool = True, residual=None, ids=None,
               weights=None, y=None, workspace=None, stream=None):
     """The whole layer: moe_route, then w4a16_moe_experts.  Returns (y, ids, weights)."""
-    dev, T, H = _tokens(x)
+    idx = _device_of(x, "x")
+    away = _elsewhere(idx, stream)
+    if away is not None:
+        with away:
+            return w4a16_moe(x, w_router, gate_up, down, I, topk, renormalize=renormalize, residual=residual, ids=ids,
+                             weights=weights, y=y, workspace=workspace)
+    xp, T, H = _tokens(x, idx)
     E = w_router.shape[0]
-    _need(w_router, "w_router", dev, torch.bfloat16, shape=(E, H))
-    with _on(dev, stream):
-        ids, weights = _choices(dev, T, topk, ids, weights)
-        y, workspace, ws_bytes = _expert_tensors(dev, T, E, H, I, topk, gate_up, down, residual, y, workspace)
-        _check(lib().w4a16_moe(x.data_ptr(), w_router.data_ptr(), gate_up[0].data_ptr(), gate_up[1].data_ptr(),
-                               down[0].data_ptr(), down[1].data_ptr(), _ptr(residual), y.data_ptr(), ids.data_ptr(),
-                               weights.data_ptr(), T, E, H, I, topk, int(renormalize), workspace.data_ptr(), ws_bytes,
-                               _stream(stream)), "w4a16_moe")
+    rp = _need_shape(w_router, "w_router", idx, torch.bfloat16, (E, H))
+    ids, weights, ip, wp = _choices(x, idx, T, topk, ids, weights)
+    y, workspace, ptrs, ws = _experts(x, idx, T, E, H, I, topk, gate_up, down, residual, y, workspace)
+    _check(lib().w4a16_moe(xp, rp, *ptrs, ip, wp, T, E, H, I, topk, 1 if renormalize else 0, *ws, _handle(idx)),
+           "w4a16_moe")
     return y, ids, weights
 
 

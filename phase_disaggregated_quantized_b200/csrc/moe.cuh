@@ -6,16 +6,20 @@
 //   h[t, j]      = silu(Wg[e] x[t]) * (Wu[e] x[t]),   e = ids[t, j]
 //   y[t]         = residual[t] + sum_j Wd[e] (w[t, j] h[t, j])
 //
-// Three launches chained by programmatic dependent launch: the router, gate and
-// up, down.  The experts are in the packed form of the decode GEMM (units of 32
-// rows x 128 k), gate and up rows in turn by 16, so that one unit holds 16 gate
-// rows (MMA tile 0) and the matching 16 up rows (tile 1) and a lane has both
-// halves of its h.  Weights are read from memory once per expert and eight of
-// its tokens; which experts those are is known only on the device, so each CTA
-// first sorts the (token, choice) pairs by expert into segments of at most
-// eight tokens (one MMA column each).
+// The router alone is one cluster of CTAs; the experts, with or without the
+// router before them, are one cooperative launch: a CTA per SM, phases apart by
+// grid barriers (router | selection, gate and up | down).  The experts are in the
+// packed form of the decode GEMM (units of 32 rows x 128 k), gate and up rows in
+// turn by 16, so that one unit holds 16 gate rows (MMA tile 0) and the matching
+// 16 up rows (tile 1) and a lane has both halves of its h.  Weights are read from
+// memory once per expert and eight of its tokens; which experts those are is
+// known only on the device, so each CTA first sorts the (token, choice) pairs by
+// expert into segments of at most eight tokens (one MMA column each).
 #pragma once
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
+#include <type_traits>
+#include <utility>
 #include "epilogue.cuh"
 #include "ptx.cuh"
 #include "w4a16_gemm.cuh"
@@ -29,9 +33,12 @@ constexpr int kMaxExperts = 512;
 constexpr int kMaxPairs = kMaxTokens * kMaxTopk;
 
 // ------------------------------------------------------------------ router
-constexpr int RCS = 8;              // CTAs per cluster: K is split over them
+constexpr int RCS = 16;             // CTAs per cluster: K is split over them
 constexpr int RWARPS = 16;
 constexpr int RTHREADS = RWARPS * 32;
+constexpr int RCHUNK = 8;           // 64-wide k blocks of x staged at a time
+constexpr int RXROW = RCHUNK * 128 + 16;                               // bytes of a staged row (padded: no bank conflicts)
+constexpr int RMINE = kMaxTokens / RCS;                                // tokens that one CTA selects for
 
 struct RouteShape {
   int etiles, ksub;                 // 16-expert tiles; how many warps share a tile's K range
@@ -41,12 +48,18 @@ struct RouteShape {
   }
   __host__ __device__ int e16() const { return etiles * 16; }
   __host__ __device__ int plane() const { return kMaxTokens * e16(); }              // floats
-  __host__ __device__ int smem() const { return 4 * (ksub * plane() + (kMaxTokens / RCS) * e16()); }
+  __host__ __device__ int smem() const { return 4 * (ksub * plane() + RMINE * e16()) + kMaxTokens * RXROW; }
+  // The planes are largest for the most experts (one plane) or just under
+  // RWARPS expert tiles' worth of rows (at most RWARPS tiles over all planes).
+  static constexpr int max_smem() {
+    return 4 * (kMaxTokens * kMaxExperts + RMINE * kMaxExperts) + kMaxTokens * RXROW;
+  }
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(w4a16::map_to_rank(saddr, rank)) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t saddr, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(w4a16::map_to_rank(saddr, rank)) : "memory");
   return v;
 }
 // Unsigned order of the result = order of the logits; every NaN is above all
@@ -57,12 +70,83 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_logit(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);       // NaN stays a NaN
+}
+
+// One warp: the topk of E <= 32 KPL logits (lane: l[i] of expert lane + 32 i) and
+// their weights; lane j < topk receives the j-th.
+template <int KPL>
+__device__ __forceinline__ void select_topk(const float (&l)[KPL], uint32_t E, uint32_t topk, bool renorm, uint32_t lane,
+                                            uint32_t& id, float& weight) {
+  uint32_t key[KPL], mine = 0, top = 0;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) key[i] = lane + 32 * i < E ? order_key(l[i]) : 0u;
+  id = 0;
+  for (uint32_t j = 0; j < topk; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < KPL; ++i) best = max(best, key[i]);
+    best = __reduce_max_sync(0xFFFFFFFFu, best);
+    uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = KPL - 1; i >= 0; --i) at = key[i] == best ? lane + 32 * i : at;   // the lowest
+    at = __reduce_min_sync(0xFFFFFFFFu, at);
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) key[i] = at == lane + 32 * i ? 0u : key[i];
+    if (j == 0) top = best;
+    if (lane == j) {
+      id = at;
+      mine = best;
+    }
+  }
+  const float first = key_logit(top);
+  const float e = lane < topk ? expf(key_logit(mine) - first) : 0.f;
+  float sum = e;
+  if (!renorm) {
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i)
+      if (lane + 32 * i < E) sum += expf(l[i] - first);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  weight = e / sum;
+}
+
+// The same with the logits summed over `planes` arrays, `pitch` floats apart.
+// `load` reads one float; the loads of a plane do not wait for one another.
+template <typename Load>
+__device__ __forceinline__ void select_experts(const float* l, uint32_t planes, size_t pitch, Load load, uint32_t E,
+                                               uint32_t topk, bool renorm, uint32_t lane, uint32_t& id, float& weight) {
+  auto with = [&](auto kpl) {
+    constexpr int KPL = decltype(kpl)::value;
+    float sum[KPL] = {};
+    constexpr uint32_t PL = KPL <= 4 ? 4 : 1;
+    for (uint32_t s = 0; s < planes; s += PL) {
+      float v[PL][KPL];
+#pragma unroll
+      for (uint32_t k = 0; k < PL; ++k)
+#pragma unroll
+        for (int i = 0; i < KPL; ++i) v[k][i] = s + k < planes && lane + 32 * i < E ? load(l + (s + k) * pitch + lane + 32 * i) : 0.f;
+#pragma unroll
+      for (uint32_t k = 0; k < PL; ++k)
+#pragma unroll
+        for (int i = 0; i < KPL; ++i) sum[i] += v[k][i];
+    }
+    select_topk<KPL>(sum, E, topk, renorm, lane, id, weight);
+  };
+  if (E <= 128) with(std::integral_constant<int, 4>());
+  else with(std::integral_constant<int, kMaxExperts / 32>());
+}
+
 // One cluster per 32 tokens.  CTA r multiplies the r-th part of K for all
 // experts and tokens with m16n8k16 MMAs (experts as rows, tokens as columns),
 // each MMA starting from zero and added in FP32, so that no long chain of
 // tensor-core additions truncates.  The partial logits stay in shared memory;
-// after a cluster barrier CTA r adds, in rank order, those of the tokens
-// r, r + 8, ... and one warp per token selects.
+// after a cluster barrier CTA r adds, in a fixed order, those of the tokens
+// r, r + 16 and one warp per token selects.  The first router weights are
+// requested before the wait on the preceding kernel.
 __global__ void __launch_bounds__(RTHREADS, 1)
 route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ wr, uint32_t T, uint32_t E,
              uint32_t H, uint32_t topk, uint32_t renorm, int32_t* __restrict__ ids, float* __restrict__ weights) {
@@ -74,124 +158,185 @@ route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restric
   const uint32_t t0 = w4a16::cluster_id() * kMaxTokens, nt = min((uint32_t)kMaxTokens, T - t0);
   const uint32_t nblk = H / 64, b0 = nblk * rank / RCS, b1 = nblk * (rank + 1) / RCS;
   const uint32_t ntile = (nt + 7) / 8;
+  float* logits = rsm + ksub * plane;                                  // [RMINE][e16], this CTA's tokens
+  uint8_t* xs = reinterpret_cast<uint8_t*>(logits + RMINE * e16);
+  const uint32_t per = min((uint32_t)sh.etiles, (uint32_t)RWARPS);     // warps side by side over the expert tiles
+  const uint32_t ks = warp / per, et0 = warp % per;
+  const bool active = ks < ksub;
 
+  // This warp's steps over a chunk: for each of its expert tiles, its blocks of
+  // the chunk.  A step's two expert rows of this lane are requested four steps ahead.
+  uint4 a[4][4];
+  uint32_t c0 = b0, k0 = 0, k1 = 0, le = 0, lb = 0;                    // le, lb: the step to be requested
+  auto load_a = [&](uint4 (&d)[4]) {
+    const uint32_t r_lo = min(le * 16 + g, E - 1), r_hi = min(le * 16 + g + 8, E - 1);   // rows past E: never selected
+    const uint4* lo = reinterpret_cast<const uint4*>(wr + (size_t)r_lo * H + 16 * c) + 8 * (size_t)lb;
+    const uint4* hi = reinterpret_cast<const uint4*>(wr + (size_t)r_hi * H + 16 * c) + 8 * (size_t)lb;
+    d[0] = __ldg(lo);
+    d[1] = __ldg(lo + 1);
+    d[2] = __ldg(hi);
+    d[3] = __ldg(hi + 1);
+    if (++lb == k1) {
+      lb = k0;
+      le += per;
+    }
+  };
+  uint32_t steps = 0;
+  auto begin_chunk = [&]() {
+    const uint32_t n = min((uint32_t)RCHUNK, b1 - c0);
+    k0 = c0 + n * ks / ksub;
+    k1 = c0 + n * (ks + 1) / ksub;
+    le = et0;
+    lb = k0;
+    steps = active ? (k1 - k0) * (((uint32_t)sh.etiles - et0 + per - 1) / per) : 0u;
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+      if (i < steps) load_a(a[i]);
+  };
+  begin_chunk();
   grid_dependency_wait();
   grid_launch_dependents();
-  const uint32_t per = sh.etiles >= RWARPS ? RWARPS : sh.etiles;       // warps side by side over the expert tiles
-  const uint32_t ks = warp / per;
-  if (ks < ksub) {
-    const uint32_t k0 = b0 + (b1 - b0) * ks / ksub, k1 = b0 + (b1 - b0) * (ks + 1) / ksub;
-    for (uint32_t et = warp % per; et < (uint32_t)sh.etiles; et += per) {
-      float acc[4][4] = {};
-      const uint32_t r_lo = min(et * 16 + g, E - 1), r_hi = min(et * 16 + g + 8, E - 1);   // rows past E: not selected
-      const uint4* a_lo = reinterpret_cast<const uint4*>(wr + (size_t)r_lo * H + 16 * c);
-      const uint4* a_hi = reinterpret_cast<const uint4*>(wr + (size_t)r_hi * H + 16 * c);
-      const uint4* bx[4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-        bx[n] = reinterpret_cast<const uint4*>(x + (size_t)(t0 + min(8u * n + g, nt - 1)) * H + 16 * c);
-#pragma unroll 2
-      for (uint32_t b = k0; b < k1; ++b) {
-        const uint4 l0 = __ldg(a_lo + 8 * b), l1 = __ldg(a_lo + 8 * b + 1);
-        const uint4 h0 = __ldg(a_hi + 8 * b), h1 = __ldg(a_hi + 8 * b + 1);
-        const uint32_t a[4][4] = {{l0.x, h0.x, l0.y, h0.y}, {l0.z, h0.z, l0.w, h0.w},
-                                  {l1.x, h1.x, l1.y, h1.y}, {l1.z, h1.z, l1.w, h1.w}};
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-          if ((uint32_t)n < ntile) {
-            const uint4 q0 = __ldg(bx[n] + 8 * b), q1 = __ldg(bx[n] + 8 * b + 1);
-            float d[4][4];
-            w4a16::mma_z(d[0], a[0], q0.x, q0.y);
-            w4a16::mma_z(d[1], a[1], q0.z, q0.w);
-            w4a16::mma_z(d[2], a[2], q1.x, q1.y);
-            w4a16::mma_z(d[3], a[3], q1.z, q1.w);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] += (d[0][i] + d[1][i]) + (d[2][i] + d[3][i]);
-          }
-      }
+  do {
+    const uint32_t n = min((uint32_t)RCHUNK, b1 - c0), row4 = n * 8;   // 16-byte words of a row
+    for (uint32_t i = threadIdx.x; i < nt * row4; i += RTHREADS) {
+      const uint32_t t = i / row4, w = i - t * row4;
+      *reinterpret_cast<uint4*>(xs + t * RXROW + w * 16) =
+          __ldg(reinterpret_cast<const uint4*>(x + (size_t)(t0 + t) * H + (size_t)c0 * 64) + w);
+    }
+    __syncthreads();
+    float acc[4][4] = {};
+    uint32_t et = et0, b = k0;
+    auto flush = [&]() {                                               // the partial logits of tile et
       float* p = rsm + ks * plane + et * 16 + g;
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-        if ((uint32_t)n < ntile) {
-          p[(8 * n + 2 * c) * e16] = acc[n][0];
-          p[(8 * n + 2 * c + 1) * e16] = acc[n][1];
-          p[(8 * n + 2 * c) * e16 + 8] = acc[n][2];
-          p[(8 * n + 2 * c + 1) * e16 + 8] = acc[n][3];
+      for (int m = 0; m < 4; ++m)
+        if ((uint32_t)m < ntile)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float* q = p + (8 * m + 2 * c + (e & 1)) * e16 + (e & 2) * 4;
+            *q = c0 == b0 ? acc[m][e] : *q + acc[m][e];
+            acc[m][e] = 0.f;
+          }
+    };
+    for (uint32_t s = 0; s < steps; s += 4) {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i)
+        if (s + i < steps) {
+          const uint4 l0 = a[i][0], l1 = a[i][1], h0 = a[i][2], h1 = a[i][3];
+          const uint32_t f[4][4] = {{l0.x, h0.x, l0.y, h0.y}, {l0.z, h0.z, l0.w, h0.w},
+                                    {l1.x, h1.x, l1.y, h1.y}, {l1.z, h1.z, l1.w, h1.w}};
+          if (s + i + 4 < steps) load_a(a[i]);
+          // Columns past the last token hold whatever was staged there; nothing reads them.
+          const uint8_t* xb = xs + g * RXROW + (b - c0) * 128 + 32 * c;
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if ((uint32_t)m < ntile) {
+              const uint4 q0 = *reinterpret_cast<const uint4*>(xb + m * 8 * RXROW);
+              const uint4 q1 = *reinterpret_cast<const uint4*>(xb + m * 8 * RXROW + 16);
+              float d[4][4];
+              w4a16::mma_z(d[0], f[0], q0.x, q0.y);
+              w4a16::mma_z(d[1], f[1], q0.z, q0.w);
+              w4a16::mma_z(d[2], f[2], q1.x, q1.y);
+              w4a16::mma_z(d[3], f[3], q1.z, q1.w);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[m][e] += (d[0][e] + d[1][e]) + (d[2][e] + d[3][e]);
+            }
+          if (++b == k1) {
+            flush();
+            b = k0;
+            et += per;
+          }
         }
     }
-  }
+    if (active && steps == 0 && c0 == b0)                              // no block of K is this warp's
+      for (; et < (uint32_t)sh.etiles; et += per) flush();
+    c0 += n;
+    if (c0 < b1) {
+      __syncthreads();                                                 // the staged rows were read
+      begin_chunk();
+    }
+  } while (c0 < b1);
   w4a16::cluster_arrive();
   w4a16::cluster_wait();
-  float* logits = rsm + ksub * plane;                                  // [4][e16], this CTA's tokens
+  // Four lanes per four logits, each lane the partials of RCS / 4 CTAs.
   const uint32_t mine = nt > rank ? (nt - rank + RCS - 1) / RCS : 0u;
-  for (uint32_t i = threadIdx.x; i < mine * e16; i += RTHREADS) {
-    const uint32_t q = i / e16, e = i - q * e16;
-    const uint32_t a = smem_addr(rsm + (rank + RCS * q) * e16 + e);
-    float s = 0.f;
-    for (uint32_t k = 0; k < ksub; ++k)
+  for (uint32_t i = threadIdx.x >> 2; i < mine * e16 / 4; i += RTHREADS / 4) {
+    const uint32_t q = i / (e16 / 4), e = 4 * (i - q * (e16 / 4));
+    const uint32_t at = smem_addr(rsm + (rank + RCS * q) * e16 + e), r0 = (threadIdx.x & 3u) * (RCS / 4);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t k = 0; k < ksub; ++k) {
+      float4 p[RCS / 4];
 #pragma unroll
-      for (uint32_t r = 0; r < RCS; ++r) s += ld_cluster_f32(a + 4 * k * plane, r);
-    logits[q * e16 + e] = s;
+      for (uint32_t r = 0; r < RCS / 4; ++r) p[r] = ld_cluster_f32x4(at + 4 * k * plane, r0 + r);
+#pragma unroll
+      for (uint32_t r = 0; r < RCS / 4; ++r) { v.x += p[r].x; v.y += p[r].y; v.z += p[r].z; v.w += p[r].w; }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const uint32_t quad = 0xFu << (lane & 28u);
+      v.x += __shfl_xor_sync(quad, v.x, o);
+      v.y += __shfl_xor_sync(quad, v.y, o);
+      v.z += __shfl_xor_sync(quad, v.z, o);
+      v.w += __shfl_xor_sync(quad, v.w, o);
+    }
+    if ((threadIdx.x & 3u) == 0) *reinterpret_cast<float4*>(logits + q * e16 + e) = v;
   }
+  __syncwarp();
   w4a16::cluster_arrive();                                             // every CTA's partials were read
   __syncthreads();
   if (warp < mine) {
     const float* l = logits + warp * e16;
     const uint32_t t = t0 + rank + RCS * warp;
-    uint32_t key[kMaxExperts / 32];
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) key[i] = lane + 32 * i < E ? order_key(l[lane + 32 * i]) : 0u;
-    uint32_t chosen = 0;
-    for (uint32_t j = 0; j < topk; ++j) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int i = 0; i < kMaxExperts / 32; ++i) best = max(best, key[i]);
-      best = __reduce_max_sync(0xFFFFFFFFu, best);
-      uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-      for (int i = kMaxExperts / 32 - 1; i >= 0; --i) at = key[i] == best ? lane + 32 * i : at;   // the lowest
-      at = __reduce_min_sync(0xFFFFFFFFu, at);
-#pragma unroll
-      for (int i = 0; i < kMaxExperts / 32; ++i) key[i] = at == lane + 32 * i ? 0u : key[i];
-      if (lane == j) chosen = at;
-    }
-    const float top = l[__shfl_sync(0xFFFFFFFFu, chosen, 0)];
-    float e = lane < topk ? expf(l[chosen] - top) : 0.f;
-    float sum = e;
-    if (!renorm) {
-      sum = 0.f;
-      for (uint32_t i = lane; i < E; i += 32) sum += expf(l[i] - top);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    uint32_t id;
+    float w;
+    select_experts(l, 1, 0, [](const float* q) { return *q; }, E, topk, renorm != 0, lane, id, w);
     if (lane < topk) {
-      ids[(size_t)t * topk + lane] = (int32_t)chosen;
-      weights[(size_t)t * topk + lane] = e / sum;
+      ids[(size_t)t * topk + lane] = (int32_t)id;
+      weights[(size_t)t * topk + lane] = w;
     }
   }
   w4a16::cluster_wait();
 }
 
 // ------------------------------------------------------------------ segments
-constexpr int EWARPS = 8;
+constexpr int EWARPS = 16;
 constexpr int ETHREADS = EWARPS * 32;
-constexpr int COLS = 8;             // tokens of one segment
+constexpr uint32_t COLS = 8;        // tokens of one segment
+
+// n / d for n < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d), 2^l >= d,
+// is at most 2^l / 2^(31 + l) too large relative to 1 / d, less than 1 / n.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  __host__ explicit FastDiv(uint32_t d_) : d(d_) {
+    uint32_t l = 0;
+    while (l < 31 && (1u << l) < d) ++l;
+    mul = (uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d);
+    shift = 31 + l;
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)(((uint64_t)n * mul) >> shift); }
+};
 
 struct ExpertParams {
   const __nv_bfloat16* x;           // [T, H]
-  const int32_t* ids;               // [T, topk]
-  const float* weights;             // [T, topk]
+  int32_t* ids;                     // [T, topk]: read, or written by the router phase
+  float* weights;                   // [T, topk]
   const uint8_t* gu_codes;          // E x [2I, H] packed
   const uint8_t* gu_scales;
   const uint8_t* d_codes;           // E x [H, I] packed
   const uint8_t* d_scales;
   const __nv_bfloat16* residual;    // [T, H] or NULL
   __nv_bfloat16* y;                 // [T, H]
-  __nv_bfloat16* h_hi;              // [T * topk, I]
-  __nv_bfloat16* h_lo;
+  __nv_bfloat16* h;                 // [2][T * topk, I]: high halves, then low halves; see h_at
   uint32_t* tickets;                // [H / 32]
   float* partial;                   // [2 gridDim][T][32]
   uint32_t T, E, H, I, topk;
+  uint32_t stage;                   // all of h fits in shared memory
+  FastDiv by_topk, by_grid, by_g, by_rtiles;   // topk, gridDim, H / 128, I / 16
+  // the router phase
+  const __nv_bfloat16* wr;          // [E, H]
+  float* logits;                    // [slices][T][16 etiles] partial sums
+  uint32_t renorm, etiles, slices;
 };
 
 struct Plan {
@@ -200,42 +345,82 @@ struct Plan {
   int32_t id[kMaxPairs];
   float w[kMaxPairs];
   uint16_t first[kMaxExperts];      // first slot of each expert
-  uint16_t pair[kMaxPairs];         // slot (sorted by expert, then token) -> pair t * topk + j
+  uint16_t pair[kMaxPairs];         // slot (the tokens of one expert together) -> pair t * topk + j
   uint16_t seg_e[kMaxPairs], seg_s[kMaxPairs];   // segment -> expert, first slot
-  uint8_t seg_n[kMaxPairs];         // its tokens, 1 .. 8
+  uint8_t seg_n[kMaxPairs];         // its tokens, 1 .. COLS
+  uint8_t token[kMaxPairs];         // slot -> token
   uint32_t warp_sum[EWARPS];
   uint32_t segments;
 };
 
-// Sorts the pairs by expert.  An id outside [0, E) is no choice; an expert that
-// a token names twice counts once, with the sum of the weights (the same sum of
-// products), so that a segment never holds a token twice.  Called by the whole CTA.
+// Sorts the pairs of pl.id / pl.w by expert into segments of at most COLS tokens
+// of one expert.  An id outside [0, E) is no choice; an expert that a token names
+// twice counts once, with the sum of the weights (the same sum of products), so
+// that a segment never holds a token twice.  Called by the whole CTA, pl.id and
+// pl.w filled and visible.
 __device__ __forceinline__ void build_plan(Plan& pl, const ExpertParams& p) {
   const uint32_t P = p.T * p.topk, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
-  for (uint32_t e = tid; e < p.E; e += ETHREADS) pl.mask[e] = 0u;
-  for (uint32_t i = tid; i < P; i += ETHREADS) {
-    pl.id[i] = p.ids[i];
-    pl.w[i] = p.weights[i];
+  if (P <= 32) {                    // one warp, a pair per lane; experts in the order of their first pair
+    if (warp == 0) {
+      const int32_t id = lane < P ? pl.id[lane] : -1;
+      const uint32_t t = p.by_topk.div(lane);
+      const bool valid = lane < P && (uint32_t)id < p.E;
+      const uint32_t lt = (1u << lane) - 1u;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, valid ? id : -1 - (int32_t)lane);
+      const uint32_t ends = (t + 1) * p.topk;                          // the token's lanes [t topk, ends)
+      const uint32_t own = same & (ends >= 32 ? 0xFFFFFFFFu : (1u << ends) - 1u) & ~((1u << (t * p.topk)) - 1u);
+      const bool first = valid && (own & lt) == 0;
+      float s = lane < P ? pl.w[lane] : 0.f;
+      if (first)
+        for (uint32_t m = own & ~lt & ~(1u << lane); m; m &= m - 1) s += pl.w[__ffs(m) - 1];
+      const uint32_t group = same & __ballot_sync(0xFFFFFFFFu, first);  // the expert's pairs that count
+      const uint32_t n = __popc(group), within = __popc(group & lt);
+      const bool leads = first && within == 0;
+      // Slots in the low half, segments in the high half of one sum over the leaders.
+      uint32_t inc = leads ? n | ((n + COLS - 1) / COLS) << 16 : 0u;
+      const uint32_t add = inc;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= (uint32_t)o) inc += v;
+      }
+      const uint32_t base = __shfl_sync(0xFFFFFFFFu, inc - add, group ? __ffs(group) - 1 : 0);
+      if (first) {
+        const uint32_t slot = (base & 0xFFFFu) + within;
+        pl.pair[slot] = (uint16_t)lane;
+        pl.token[slot] = (uint8_t)t;
+        pl.pw[lane] = s;
+        if (within % COLS == 0) {
+          const uint32_t seg = (base >> 16) + within / COLS;
+          pl.seg_e[seg] = (uint16_t)id;
+          pl.seg_s[seg] = (uint16_t)slot;
+          pl.seg_n[seg] = (uint8_t)min(COLS, n - within);
+        }
+      }
+      if (lane == 31) pl.segments = inc >> 16;
+    }
+    __syncthreads();
+    return;
   }
+  static_assert(kMaxExperts == ETHREADS && kMaxPairs == ETHREADS, "an expert and a pair per thread");
+  pl.mask[tid] = 0u;
   __syncthreads();
-  for (uint32_t i = tid; i < P; i += ETHREADS) {
-    const uint32_t t = i / p.topk, j0 = t * p.topk;
-    const int32_t id = pl.id[i];
-    bool first = (uint32_t)id < p.E;
-    for (uint32_t j = j0; j < i; ++j) first = first && pl.id[j] != id;
-    float s = pl.w[i];
-    for (uint32_t j = i + 1; j < j0 + p.topk; ++j)
+  const uint32_t t = p.by_topk.div(tid), j0 = t * p.topk;
+  const int32_t id = tid < P ? pl.id[tid] : -1;
+  bool first = (uint32_t)id < p.E;
+  if (first) {
+    float s = pl.w[tid];
+#pragma unroll 4
+    for (uint32_t j = j0; j < tid; ++j) first &= pl.id[j] != id;
+#pragma unroll 4
+    for (uint32_t j = tid + 1; j < j0 + p.topk; ++j)
       if (pl.id[j] == id) s += pl.w[j];
-    pl.pw[i] = s;
+    pl.pw[tid] = s;
     if (first) atomicOr(&pl.mask[id], 1u << t);
   }
   __syncthreads();
-  // Two experts per thread: slots in the low half, segments in the high half of one sum.
-  static_assert(kMaxExperts == 2 * ETHREADS, "two experts per thread");
-  const uint32_t m0 = 2 * tid < p.E ? pl.mask[2 * tid] : 0u, m1 = 2 * tid + 1 < p.E ? pl.mask[2 * tid + 1] : 0u;
-  const uint32_t n0 = __popc(m0), n1 = __popc(m1), s0 = (n0 + COLS - 1) / COLS, s1 = (n1 + COLS - 1) / COLS;
-  const uint32_t own = (n0 + n1) | ((s0 + s1) << 16);
-  uint32_t inc = own;
+  const uint32_t n = __popc(pl.mask[tid]), add = n | ((n + COLS - 1) / COLS) << 16;
+  uint32_t inc = add;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
@@ -243,67 +428,102 @@ __device__ __forceinline__ void build_plan(Plan& pl, const ExpertParams& p) {
   }
   if (lane == 31) pl.warp_sum[warp] = inc;
   __syncthreads();
-  uint32_t before = inc - own;
+  uint32_t before = inc - add;
   for (uint32_t w = 0; w < warp; ++w) before += pl.warp_sum[w];
-  uint32_t slot = before & 0xFFFFu, seg = before >> 16;
-#pragma unroll
-  for (uint32_t k = 0; k < 2; ++k) {
-    const uint32_t e = 2 * tid + k, n = k ? n1 : n0;
-    if (e < p.E) pl.first[e] = (uint16_t)slot;
-    for (uint32_t q = 0; q < n; q += COLS, ++seg) {
-      pl.seg_e[seg] = (uint16_t)e;
-      pl.seg_s[seg] = (uint16_t)(slot + q);
-      pl.seg_n[seg] = (uint8_t)min((uint32_t)COLS, n - q);
-    }
-    slot += n;
+  const uint32_t slot = before & 0xFFFFu;
+  uint32_t seg = before >> 16;
+  pl.first[tid] = (uint16_t)slot;
+  for (uint32_t q = 0; q < n; q += COLS, ++seg) {
+    pl.seg_e[seg] = (uint16_t)tid;
+    pl.seg_s[seg] = (uint16_t)(slot + q);
+    pl.seg_n[seg] = (uint8_t)min(COLS, n - q);
   }
   if (tid == ETHREADS - 1) pl.segments = seg;
   __syncthreads();
-  for (uint32_t i = tid; i < P; i += ETHREADS) {
-    const uint32_t t = i / p.topk, j0 = t * p.topk;
-    const int32_t id = pl.id[i];
-    bool first = (uint32_t)id < p.E;
-    for (uint32_t j = j0; j < i; ++j) first = first && pl.id[j] != id;
-    if (first) pl.pair[pl.first[id] + __popc(pl.mask[id] & ((1u << t) - 1u))] = (uint16_t)i;
+  if (first) {
+    const uint32_t k = pl.first[id] + __popc(pl.mask[id] & ((1u << t) - 1u));
+    pl.pair[k] = (uint16_t)tid;
+    pl.token[k] = (uint8_t)t;
   }
   __syncthreads();
 }
 
-// ------------------------------------------------------------------ one unit
+// ------------------------------------------------------------------ streaming the units
+// Each warp keeps RING units in flight into its own shared-memory slots with
+// 16-byte cp.async copies.  A lane copies exactly the words that it reads
+// itself, so its own wait is all the synchronisation there is.
+constexpr int SLOT = 2048 + 32 * 8;                      // codes, then each lane's four row scales
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <int RING>
+struct Ring {
+  uint32_t base, at;                                     // shared addresses: this lane's words of slot 0 and of the current slot
+  const uint8_t *codes, *scales;                         // this lane's words of the next unit
+  uint32_t lane;
+
+  __device__ __forceinline__ void init(void* smem, uint32_t warp, uint32_t lane_) {
+    lane = lane_;
+    base = at = smem_addr(smem) + warp * RING * SLOT + 16 * lane;
+  }
+  __device__ __forceinline__ void locate(const uint8_t* c, const uint8_t* s, size_t unit) {
+    codes = c + unit * 2048 + 16 * lane;
+    scales = s + unit * 64 + 8 * (lane >> 2);
+  }
+  __device__ __forceinline__ void copy() {               // the next unit into the current slot
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cp_async16(at + 512 * i, codes + 512 * i);
+    cp_async8(at + 2048 - 8 * lane, scales);
+    codes += 2048;
+    scales += 64;
+  }
+  __device__ __forceinline__ void step() { at = at == base + (RING - 1) * SLOT ? base : at + SLOT; }
+};
+
 struct Weights {                    // one unit's codes of this lane and its four row scales
   uint4 q[4];
   uint2 s;
-};
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-__device__ __forceinline__ void load_unit(Weights& w, const uint8_t* codes, const uint8_t* scales, size_t unit,
-                                          uint32_t lane) {
-  const uint8_t* c = codes + unit * 2048 + lane * 16;
+  __device__ __forceinline__ void read(uint32_t at, uint32_t lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w.q[i] = ldg_stream(c + 512 * i);
-  w.s = __ldg(reinterpret_cast<const uint2*>(scales + unit * 64 + (lane >> 2) * 8));
+    for (int i = 0; i < 4; ++i) q[i] = w4a16::lds128(at + 512 * i);
+    s = w4a16::lds64(at + 2048 - 8 * lane);
+  }
+};
+
+constexpr uint32_t kNeg136 = 0xC308C308u;                // bf16x2 (-136, -136)
+
+// -136 times the sum of each column: off[0] for column 2 c, off[1] for 2 c + 1.
+__device__ __forceinline__ void column_offsets(const uint4 (&b)[4], float (&off)[2]) {
+  const uint32_t neg[4] = {kNeg136, kNeg136, kNeg136, kNeg136};
+  float d[4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint4 q = b[j >> 1];
+    const uint32_t b0 = (j & 1) ? q.z : q.x, b1 = (j & 1) ? q.w : q.y;
+    if (j == 0) w4a16::mma_z(d, neg, b0, b1);
+    else w4a16::mma_acc(d, neg, b0, b1);
+  }
+  off[0] = d[0];
+  off[1] = d[1];
 }
 
-// d[tt] = sum over the unit's 128 k of (128 + u) b; d += -136 sum b.  NB operand
-// runs are added (the two halves of h).
-template <int NB>
-__device__ __forceinline__ void unit_products(const Weights& w, const uint4 (&b)[NB][4], float (&d)[2][4]) {
-  constexpr uint32_t kNeg136 = 0xC308C308u;              // bf16x2 (-136, -136)
+// acc[n][tt] += scale * (sum of the unit's codes times the columns b[n] - 8 times their
+// sum).  The codes enter as 128 + u; what that adds is taken off by `off` (GIVEN:
+// column_offsets of b[n], the first products' C operand) or by a third chain of products
+// next to those of the two row tiles, whose latency it shares.
+template <bool GIVEN, int NB>
+__device__ __forceinline__ void unit_products(const Weights& w, const uint4 (&b)[NB][4], const float (&off)[NB][2],
+                                              float (&acc)[NB][2][4]) {
   const uint32_t neg[4] = {kNeg136, kNeg136, kNeg136, kNeg136};
-  float off[4];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const uint4 q = b[n][j >> 1];
-      const uint32_t b0 = (j & 1) ? q.z : q.x, b1 = (j & 1) ? q.w : q.y;
-      if (j == 0 && n == 0) w4a16::mma_z(off, neg, b0, b1);
-      else w4a16::mma_acc(off, neg, b0, b1);
-    }
+  float o[NB][4], d[NB][2][4];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint4 v = w.q[j >> 1];
@@ -314,289 +534,561 @@ __device__ __forceinline__ void unit_products(const Weights& w, const uint4 (&b)
     for (int n = 0; n < NB; ++n) {
       const uint4 q = b[n][j >> 1];
       const uint32_t b0 = (j & 1) ? q.z : q.x, b1 = (j & 1) ? q.w : q.y;
-      if (j == 0 && n == 0) {
-        w4a16::mma_z(d[0], a0, b0, b1);
-        w4a16::mma_z(d[1], a1, b0, b1);
-      } else {
-        w4a16::mma_acc(d[0], a0, b0, b1);
-        w4a16::mma_acc(d[1], a1, b0, b1);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    d[0][i] += off[i];
-    d[1][i] += off[i];
-  }
-}
-__device__ __forceinline__ void add_scaled(float (&acc)[2][4], const float (&d)[2][4], uint2 s) {
-#pragma unroll
-  for (int tt = 0; tt < 2; ++tt) {
-    const uint32_t v = tt ? s.y : s.x;
-    const float lo = bf16_lo(v), hi = bf16_hi(v);
-    acc[tt][0] = __fmaf_rn(lo, d[tt][0], acc[tt][0]);
-    acc[tt][1] = __fmaf_rn(lo, d[tt][1], acc[tt][1]);
-    acc[tt][2] = __fmaf_rn(hi, d[tt][2], acc[tt][2]);
-    acc[tt][3] = __fmaf_rn(hi, d[tt][3], acc[tt][3]);
-  }
-}
-
-// ------------------------------------------------------------------ gate and up
-// A tile is one segment x 16 h columns (one packed row tile: 16 gate and 16 up
-// rows), G = H / 128 units.  A CTA owns whole tiles (segment-major, so that it
-// stays with one expert's rows of x), its warps equal runs of their units; a
-// tile inside one run is finished in registers, the others through shared memory.
-__global__ void __launch_bounds__(ETHREADS, 2) gate_up_kernel(const ExpertParams p) {
-  __shared__ Plan pl;
-  __shared__ __align__(16) float part[EWARPS][2][32 * 8];
-  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g8 = lane >> 2, c = lane & 3u;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  build_plan(pl, p);
-  for (uint32_t i = blockIdx.x * ETHREADS + threadIdx.x; i < p.H / 32; i += gridDim.x * ETHREADS) p.tickets[i] = 0u;
-  const uint32_t G = p.H / 128, rtiles = p.I / 16;
-  const uint64_t tiles = (uint64_t)pl.segments * rtiles;
-  const uint64_t T0 = tiles * blockIdx.x / gridDim.x, T1 = tiles * (blockIdx.x + 1) / gridDim.x;
-  const uint32_t L = (uint32_t)(T1 - T0) * G;                      // this CTA's units
-  auto cut = [&](uint32_t w) { return (uint32_t)((uint64_t)L * w / EWARPS); };
-  const uint32_t f0 = cut(warp), f1 = cut(warp + 1);
-
-  // h of one finished tile from this lane's sums: rows (h columns) g8 and g8 + 8, tokens 2c and 2c + 1.
-  auto finish = [&](const float (&acc)[2][4], uint32_t seg, uint32_t rt) {
-    const uint32_t n = pl.seg_n[seg], s = pl.seg_s[seg];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t col = 2 * c + (i & 1);
-      if (col < n) {
-        const uint32_t pr = pl.pair[s + col];
-        const float h = times_sigmoid(acc[0][i], acc[0][i]) * acc[1][i] * pl.pw[pr];
-        // Two BF16 halves carry h to 16 bits: one would add an error as large as the rounding of y.
-        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-        const size_t at = (size_t)pr * p.I + rt * 16 + g8 + ((i & 2) ? 8 : 0);
-        p.h_hi[at] = hi;
-        p.h_lo[at] = __float2bfloat16_rn(h - __bfloat162float(hi));
-      }
-    }
-  };
-
-  if (f0 < f1) {
-    const uint32_t first_tile = f0 / G;
-    uint64_t tile = T0 + first_tile;
-    uint32_t seg = (uint32_t)(tile / rtiles), rt = (uint32_t)(tile % rtiles), g = f0 % G;
-    uint32_t nseg = seg, nrt = rt, ng = g;                         // the unit being requested
-    size_t nunit = 0;
-    auto locate = [&]() { nunit = ((size_t)pl.seg_e[nseg] * rtiles + nrt) * G + ng; };
-    auto advance = [&]() {
-      ++nunit;
-      if (++ng == G) {
-        ng = 0;
-        if (++nrt == rtiles) {
-          nrt = 0;
-          if (++nseg < pl.segments) locate();
-        }
-      }
-    };
-    locate();
-    Weights wa, wb;
-    load_unit(wa, p.gu_codes, p.gu_scales, nunit, lane);
-    advance();
-    const uint4* xrow = nullptr;
-    auto row_of = [&](uint32_t s) {
-      xrow = g8 < pl.seg_n[s]
-                 ? reinterpret_cast<const uint4*>(p.x + (size_t)(pl.pair[pl.seg_s[s] + g8] / p.topk) * p.H + 32 * c)
-                 : nullptr;
-    };
-    row_of(seg);
-    float acc[2][4] = {};
-    const bool head = g != 0;
-    for (uint32_t f = f0; f < f1; ++f) {
-      if (f + 1 < f1) {
-        load_unit(wb, p.gu_codes, p.gu_scales, nunit, lane);
-        advance();
-      }
-      uint4 b[1][4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[0][i] = xrow ? __ldg(xrow + g * 16 + i) : make_uint4(0, 0, 0, 0);
-      float d[2][4];
-      unit_products<1>(wa, b, d);
-      add_scaled(acc, d, wa.s);
-      wa = wb;
-      if (++g == G) {                                              // the tile ends in this run
-        if (head && (uint32_t)(tile - T0) == first_tile) {
-          float4* q = reinterpret_cast<float4*>(part[warp][0] + lane * 8);
-          q[0] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
-          q[1] = make_float4(acc[1][0], acc[1][1], acc[1][2], acc[1][3]);
+      if (j == 0) {
+        if constexpr (GIVEN) {
+          const float c[4] = {off[n][0], off[n][1], off[n][0], off[n][1]};
+          w4a16::mma_c(d[n][0], a0, b0, b1, c);
+          w4a16::mma_c(d[n][1], a1, b0, b1, c);
         } else {
-          finish(acc, seg, rt);
+          w4a16::mma_z(d[n][0], a0, b0, b1);
+          w4a16::mma_z(d[n][1], a1, b0, b1);
+          w4a16::mma_z(o[n], neg, b0, b1);
         }
+      } else {
+        w4a16::mma_acc(d[n][0], a0, b0, b1);
+        w4a16::mma_acc(d[n][1], a1, b0, b1);
+        if constexpr (!GIVEN) w4a16::mma_acc(o[n], neg, b0, b1);
+      }
+    }
+  }
+  const float sc[4] = {bf16_lo(w.s.x), bf16_hi(w.s.x), bf16_lo(w.s.y), bf16_hi(w.s.y)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.f;
-        g = 0;
-        ++tile;
-        if (++rt == rtiles) {
-          rt = 0;
-          if (++seg < pl.segments) row_of(seg);
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[n][tt][i] = __fmaf_rn(sc[2 * tt + (i >> 1)], GIVEN ? d[n][tt][i] : d[n][tt][i] + o[n][i], acc[n][tt][i]);
+}
+
+// h is kept in the order in which the down phase reads it: inside a group of 128
+// columns, column 32 c + 8 i + e at 32 i + 8 c + e, so that the i-th 16-byte load of
+// the four lanes c takes 64 consecutive bytes.  Where the 16 columns of row tile rt
+// begin; their second half is 32 further on.
+__device__ __forceinline__ uint32_t h_at(uint32_t rt) {
+  const uint32_t k = (rt & 7u) * 16;
+  return (rt >> 3) * 128 + (k & 16u) * 4 + (k >> 5) * 8;
+}
+
+// One more part of a tile is in memory: the number of those before it.  The
+// writes of the CTA's threads, ordered before this by a CTA barrier, are released
+// with it, and the other parts' are visible after it.
+__device__ __forceinline__ uint32_t ticket(uint32_t* counter) {
+  uint32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
+}
+
+// a / b, in 32 bits where both fit (a 64-bit division is a long subroutine).
+__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
+  return ((a | b) >> 32) == 0 ? (uint64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// ------------------------------------------------------------------ the layer
+constexpr int RING = 3;
+constexpr int RING_BYTES = EWARPS * RING * SLOT;
+// Behind the ring: the down phase's per-token rows of each warp, before that the
+// gate and up phase's cut tiles (two of 16 x 8 x 2 sums per warp).
+// All of h (P pairs of I values, two halves each) goes there too when it fits
+// beside the rows of a call with the most tokens: a few tokens' h, which every
+// CTA reads whole.
+constexpr int kBehindRing = EWARPS * kMaxTokens * 32 * 4;
+constexpr bool stage_h(int64_t T, int64_t P, int64_t I) { return EWARPS * T * 32 * 4 + P * I * 4 <= kBehindRing; }
+// The gate and up phase keeps there the column offsets of up to kOffsets (segment,
+// group) pairs behind the cut tiles.
+constexpr uint32_t kOffsets = 512;
+constexpr int kCutTiles = EWARPS * 2 * 1024;
+constexpr int layer_smem(int64_t T, int64_t P, int64_t I) {
+  const int64_t rows = EWARPS * T * 32 * 4 + (stage_h(T, P, I) ? P * I * 4 : 0), gate = kCutTiles + kOffsets * 32;
+  return RING_BYTES + (int)(rows > gate ? rows : gate);
+}
+
+// One 64-wide k block of the router: 16 experts x 8 M tokens, K permuted alike in
+// both operands so that a lane's words are 32 consecutive bytes.
+template <int M>
+__device__ __forceinline__ void route_block(const uint4* lo, const uint4* hi, const uint4* const (&xb)[M], uint32_t ntile,
+                                            float (&acc)[M][4]) {
+  const uint4 l0 = __ldg(lo), l1 = __ldg(lo + 1), h0 = __ldg(hi), h1 = __ldg(hi + 1);
+  const uint32_t f[4][4] = {{l0.x, h0.x, l0.y, h0.y}, {l0.z, h0.z, l0.w, h0.w},
+                            {l1.x, h1.x, l1.y, h1.y}, {l1.z, h1.z, l1.w, h1.w}};
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+    if ((uint32_t)m < ntile) {
+      const uint4 q0 = __ldg(xb[m]), q1 = __ldg(xb[m] + 1);
+      float d[4][4];
+      w4a16::mma_z(d[0], f[0], q0.x, q0.y);
+      w4a16::mma_z(d[1], f[1], q0.z, q0.w);
+      w4a16::mma_z(d[2], f[2], q1.x, q1.y);
+      w4a16::mma_z(d[3], f[3], q1.z, q1.w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[m][e] += (d[0][e] + d[1][e]) + (d[2][e] + d[3][e]);
+    }
+}
+
+// Gate and up: a tile is one segment x 16 h columns (one packed row tile: 16 gate
+// and 16 up rows), H / 128 units.  A CTA owns whole tiles (segment-major, so that
+// it stays with one expert's rows of x), its warps equal runs of their units; a
+// tile inside one run is finished in registers, the others through shared memory.
+//
+// Down: a tile is 32 columns of y, all segments x I / 128 units.  With few units
+// a CTA takes whole tiles; else the flat sequence of units is cut into equal
+// parts, one per CTA.  A warp adds its run's products per token in its own
+// shared-memory rows, the warps' rows are added in order.  A tile that several
+// parts share is finished by the CTA that comes last (a ticket per tile), which
+// adds the parts' sums in order: nothing waits, and the result does not depend on
+// who came last.
+template <bool ROUTE>
+__global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) {
+  extern __shared__ __align__(16) uint8_t esm[];
+  __shared__ Plan pl;
+  __shared__ uint32_t last[2];
+  const auto grid = cooperative_groups::this_grid();
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g8 = lane >> 2, c = lane & 3u;
+  const uint32_t T = p.T, H = p.H, I = p.I, P = T * p.topk;
+
+  // ---- router: one CTA per 16 experts and slice of K, its warps side by side over the slice
+  if constexpr (ROUTE) {
+    float* part = reinterpret_cast<float*>(esm);                       // [EWARPS][8 ntile][16]
+    const uint32_t ntile = (T + 7) / 8, e16 = p.etiles * 16, nblk = H / 64;
+    for (uint32_t item = blockIdx.x; item < p.etiles * p.slices; item += gridDim.x) {
+      const uint32_t sl = item / p.etiles, et = item - sl * p.etiles;
+      const uint32_t s0 = nblk * sl / p.slices, s1 = nblk * (sl + 1) / p.slices;
+      const uint32_t k0 = s0 + (s1 - s0) * warp / EWARPS, k1 = s0 + (s1 - s0) * (warp + 1) / EWARPS;
+      const uint32_t r_lo = min(et * 16 + g8, p.E - 1), r_hi = min(et * 16 + g8 + 8, p.E - 1);   // rows past E: never selected
+      const uint4* lo = reinterpret_cast<const uint4*>(p.wr + (size_t)r_lo * H + 16 * c);
+      const uint4* hi = reinterpret_cast<const uint4*>(p.wr + (size_t)r_hi * H + 16 * c);
+      const uint4* xb[4];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) xb[m] = reinterpret_cast<const uint4*>(p.x + (size_t)min(8u * m + g8, T - 1) * H + 16 * c) + 8 * k0;
+      float acc[4][4] = {};
+#pragma unroll 2
+      for (uint32_t b = k0; b < k1; ++b) {
+        route_block<4>(lo + 8 * b, hi + 8 * b, xb, ntile, acc);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) xb[m] += 8;
+      }
+      float* q = part + warp * ntile * 128 + g8;
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        if ((uint32_t)m < ntile)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[(8 * m + 2 * c + (e & 1)) * 16 + (e & 2) * 4] = acc[m][e];
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < T * 16; i += ETHREADS) {
+        float v = 0.f;
+#pragma unroll
+        for (uint32_t w = 0; w < EWARPS; ++w) v += part[w * ntile * 128 + i];
+        __stcg(p.logits + ((size_t)sl * T + (i >> 4)) * e16 + et * 16 + (i & 15u), v);
+      }
+      __syncthreads();
+    }
+    grid.sync();
+    // Every CTA selects for all tokens; one CTA per token writes the result.
+    for (uint32_t t = warp; t < T; t += EWARPS) {
+      uint32_t id;
+      float w;
+      select_experts(p.logits + (size_t)t * e16, p.slices, (size_t)T * e16, [](const float* q) { return __ldcg(q); },
+                     p.E, p.topk, p.renorm != 0, lane, id, w);
+      if (lane < p.topk) {
+        pl.id[t * p.topk + lane] = (int32_t)id;
+        pl.w[t * p.topk + lane] = w;
+        if (blockIdx.x == t % gridDim.x) {
+          p.ids[t * p.topk + lane] = (int32_t)id;
+          p.weights[t * p.topk + lane] = w;
         }
       }
     }
-    if (g != 0) {                                                  // the run ends inside a tile
-      float4* q = reinterpret_cast<float4*>(part[warp][(uint32_t)(tile - T0) == first_tile ? 0 : 1] + lane * 8);
-      q[0] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
-      q[1] = make_float4(acc[1][0], acc[1][1], acc[1][2], acc[1][3]);
+  } else {
+    for (uint32_t i = threadIdx.x; i < P; i += ETHREADS) {
+      pl.id[i] = p.ids[i];
+      pl.w[i] = p.weights[i];
     }
   }
   __syncthreads();
-  for (uint32_t i = warp; i < (uint32_t)(T1 - T0); i += EWARPS) {  // tiles cut by a run's end: warps in order
-    const uint32_t tb = i * G, te = tb + G;
-    float acc[2][4] = {};
-    bool any = false;
-    for (uint32_t w = 0; w < EWARPS; ++w) {
-      const uint32_t a = cut(w), b = cut(w + 1);
-      if (a < b && a < te && b > tb && !(a <= tb && b >= te)) {
-        const float4* q = reinterpret_cast<const float4*>(part[w][a >= tb ? 0 : 1] + lane * 8);
-        const float4 v0 = q[0], v1 = q[1];
+  build_plan(pl, p);
+  const uint32_t segments = pl.segments, G = H / 128, rtiles = I / 16, Gi = I / 128, ntile = H / 32;
+  const size_t low = (size_t)P * I;                                    // from a high half of h to its low half
+
+  // ---- gate and up
+  Ring<RING> ring;
+  ring.init(esm, warp, lane);
+  {
+    float* part = reinterpret_cast<float*>(esm + RING_BYTES);          // [EWARPS][2][256]
+    // A unit of a segment with n tokens costs about kUnitCost + n: its n rows of x are
+    // read next to the weights (8192 tokens' worth of measurement: 111 us a CTA for
+    // n = 1, 122 for 4, 134 for 7).  The segments' costs are cut into equal parts; with
+    // as many slots before a segment as tokens, the cost before it is a sum of two
+    // known numbers.
+    constexpr uint32_t kUnitCost = 28;
+    const uint32_t slots = segments ? pl.seg_s[segments - 1] + pl.seg_n[segments - 1] : 0u;
+    const uint32_t cost = (kUnitCost * segments + slots) * rtiles, quot = p.by_grid.div(cost), rest = cost - quot * gridDim.x;
+    auto first_tile = [&](uint32_t b) {
+      const uint32_t at = b * quot + min(b, rest);
+      uint32_t s = 0;                                                  // segments that begin at or before `at`
+      for (uint32_t k = 0; k < segments; k += 32)
+        s += __popc(__ballot_sync(0xFFFFFFFFu, k + lane < segments && (kUnitCost * (k + lane) + pl.seg_s[k + lane]) * rtiles <= at));
+      if (s == 0 || at == cost) return segments * rtiles;
+      --s;
+      return s * rtiles + (at - (kUnitCost * s + pl.seg_s[s]) * rtiles) / (kUnitCost + pl.seg_n[s]);
+    };
+    const uint32_t T0 = first_tile(blockIdx.x), mine = first_tile(blockIdx.x + 1) - T0;
+    const uint32_t L = mine * G;                                       // this CTA's units
+    auto cut = [&](uint32_t w) { return (uint32_t)((uint64_t)L * w / EWARPS); };
+    const uint32_t f0 = cut(warp), f1 = cut(warp + 1);
+
+    // h of one finished tile from this lane's sums: rows (h columns) g8 and g8 + 8, tokens 2 c and 2 c + 1.
+    auto finish = [&](const float (&acc)[2][4], uint32_t seg, uint32_t rt) {
+      const uint32_t n = pl.seg_n[seg], s = pl.seg_s[seg];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (2 * c + k < n) {
+          const uint32_t pr = pl.pair[s + 2 * c + k];
+          const float w = pl.pw[pr];
+          __nv_bfloat16* to = p.h + (size_t)pr * I + h_at(rt) + g8;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float gate = acc[0][2 * r + k], h = times_sigmoid(gate, gate) * acc[1][2 * r + k] * w;
+            // Two BF16 halves carry h to 16 bits: one would add an error as large as the rounding of y.
+            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+            to[32 * r] = hi;
+            to[32 * r + low] = __float2bfloat16_rn(h - __bfloat162float(hi));
+          }
+        }
+    };
+    auto put = [&](const float (&acc)[2][4], uint32_t slot) {
+      float4* q = reinterpret_cast<float4*>(part + (warp * 2 + slot) * 256) + lane;
+      q[0] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+      q[32] = make_float4(acc[1][0], acc[1][1], acc[1][2], acc[1][3]);
+    };
+    const bool any = f0 < f1;
+    const uint32_t first = p.by_g.div(f0), tile0 = T0 + first, per_seg = rtiles * G;
+    uint32_t seg = p.by_rtiles.div(tile0), rt = tile0 - seg * rtiles, g = f0 - first * G;
+    uint32_t rseg = seg, rleft = per_seg - (rt * G + g), rem = f1 - f0;       // the units being requested
+    auto fill = [&]() {
+      if (rem > 0) {
+        ring.copy();
+        --rem;
+        if (--rleft == 0 && ++rseg < segments) {
+          rleft = per_seg;
+          ring.locate(p.gu_codes, p.gu_scales, (size_t)pl.seg_e[rseg] * per_seg);
+        }
+      }
+      cp_commit();
+      ring.step();
+    };
+    if (any) ring.locate(p.gu_codes, p.gu_scales, (size_t)pl.seg_e[seg] * per_seg + rt * G + g);
+#pragma unroll 1
+    for (int i = 0; i < RING; ++i) fill();
+    // A segment's rows of x; a column without a token reads the first one's (its sums are dropped).
+    auto row_of = [&](uint32_t s) {
+      const uint32_t at = pl.seg_s[s] + (g8 < pl.seg_n[s] ? g8 : 0u);
+      return reinterpret_cast<const uint4*>(p.x + (size_t)pl.token[at] * H + 32 * c);
+    };
+    auto load_x = [&](const uint4* row, uint32_t at, uint4 (&b)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = __ldg(row + at * 16 + i);
+    };
+    // While the first weights are on their way: the column offsets of this CTA's
+    // segments, which each of their row tiles needs again.
+    const uint32_t seg0 = p.by_rtiles.div(T0), nseg = mine ? p.by_rtiles.div(T0 + mine - 1) - seg0 + 1 : 0u;
+    const bool given = nseg * G <= kOffsets;
+    float2* offsets = reinterpret_cast<float2*>(esm + RING_BYTES + kCutTiles);   // [segment][group][c]
+    if (given) {
+      for (uint32_t i = warp; i < nseg * G; i += EWARPS) {
+        const uint32_t s = p.by_g.div(i);
+        uint4 b[4];
+        float off[2];
+        load_x(row_of(seg0 + s), i - s * G, b);
+        column_offsets(b, off);
+        if (g8 == 0) offsets[i * 4 + c] = make_float2(off[0], off[1]);
+      }
+      __syncthreads();
+    }
+    if (any) {
+      const uint4* row = row_of(seg);
+      const float2* offs = offsets + (seg - seg0) * G * 4 + c;
+      uint4 xv[1][4];
+      load_x(row, g, xv[0]);
+      float acc[1][2][4] = {};
+      bool head = g != 0;                                              // the first tile began in another run
+      auto run = [&](auto tab) {
+        constexpr bool GIVEN = decltype(tab)::value;
+#pragma unroll 1
+        for (uint32_t f = f0; f < f1; ++f) {
+          float off[1][2] = {};
+          if constexpr (GIVEN) {
+            const float2 o = offs[g * 4];
+            off[0][0] = o.x;
+            off[0][1] = o.y;
+          }
+          cp_wait<RING - 1>();
+          Weights w;
+          w.read(ring.at, lane);
+          unit_products<GIVEN, 1>(w, xv, off, acc);
+          const uint32_t oseg = seg, ort = rt;
+          const bool ends = ++g == G;
+          if (ends) {
+            g = 0;
+            if (++rt == rtiles) {
+              rt = 0;
+              if (++seg < segments) row = row_of(seg);
+              offs += G * 4;
+            }
+          }
+          if (f + 1 < f1) load_x(row, g, xv[0]);
+          fill();
+          if (ends) {
+            if (head) put(acc[0], 0);
+            else finish(acc[0], oseg, ort);
+            head = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[0][0][i] = acc[0][1][i] = 0.f;
+          }
+        }
+      };
+      if (given) run(std::true_type());
+      else run(std::false_type());
+      if (g != 0) put(acc[0], first == p.by_g.div(f1 - 1) ? 0 : 1);    // the run ends inside a tile
+    }
+    __syncthreads();
+    // Warp w finishes the tile that the start of its run cuts, unless an earlier
+    // warp's start cuts the same tile; the warps' parts are added in order.
+    const uint32_t tb = p.by_g.div(f0) * G, te = tb + G;
+    if (f0 != tb && f0 < L && cut(warp - 1) <= tb) {
+      float acc[2][4] = {};
+      for (uint32_t w = warp - 1; w < EWARPS && cut(w) < te; ++w) {
+        if (cut(w) == cut(w + 1)) continue;
+        const float4* q = reinterpret_cast<const float4*>(part + (w * 2 + (cut(w) >= tb ? 0 : 1)) * 256) + lane;
+        const float4 v0 = q[0], v1 = q[32];
         acc[0][0] += v0.x; acc[0][1] += v0.y; acc[0][2] += v0.z; acc[0][3] += v0.w;
         acc[1][0] += v1.x; acc[1][1] += v1.y; acc[1][2] += v1.z; acc[1][3] += v1.w;
-        any = true;
       }
+      const uint32_t tile = T0 + tb / G, seg = p.by_rtiles.div(tile);
+      finish(acc, seg, tile - seg * rtiles);
     }
-    if (any) finish(acc, (uint32_t)((T0 + i) / rtiles), (uint32_t)((T0 + i) % rtiles));
   }
-}
 
-// ------------------------------------------------------------------ down
-// A tile is 32 columns of y: all segments x I / 128 units.  The flat sequence
-// of units is cut into equal parts, one per CTA; a warp adds its run's products
-// per token in its own shared-memory rows, the warps' rows are added in order.
-// A tile that several parts share is finished by the CTA that comes last (a
-// ticket per tile), which adds the parts' sums in order: nothing waits, and the
-// result does not depend on who came last.
-__global__ void __launch_bounds__(ETHREADS, 2) down_kernel(const ExpertParams p) {
-  extern __shared__ __align__(16) float dsm[];                     // [EWARPS][T][32]
-  __shared__ Plan pl;
-  __shared__ uint32_t last;
-  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g8 = lane >> 2, c = lane & 3u;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  build_plan(pl, p);
-  const uint32_t Gi = p.I / 128, ntile = p.H / 32, outs = p.T * 32;
-  const uint64_t U = (uint64_t)pl.segments * Gi, total = U * ntile;
-  if (total == 0) {                                                // no token has an expert
-    for (size_t i = (size_t)blockIdx.x * ETHREADS + threadIdx.x; i < (size_t)p.T * p.H; i += (size_t)gridDim.x * ETHREADS)
+  // ---- down
+  for (uint32_t i = blockIdx.x * ETHREADS + threadIdx.x; i < ntile; i += gridDim.x * ETHREADS) p.tickets[i] = 0u;
+  auto arrived = grid.barrier_arrive();                                // this CTA's h is written
+  const uint32_t U = segments * Gi, outs = T * 32;
+  const uint64_t total = (uint64_t)U * ntile;
+  if (total == 0) {                                                    // no token has an expert
+    grid.barrier_wait(std::move(arrived));
+    for (size_t i = (size_t)blockIdx.x * ETHREADS + threadIdx.x; i < (size_t)T * H; i += (size_t)gridDim.x * ETHREADS)
       p.y[i] = p.residual ? p.residual[i] : __float2bfloat16_rn(0.f);
     return;
   }
-  const uint64_t parts = min((uint64_t)gridDim.x, (total + EWARPS - 1) / EWARPS);
-  if (blockIdx.x >= parts) return;
-  const uint64_t F0 = total * blockIdx.x / parts, F1 = total * (blockIdx.x + 1) / parts;
-  float* mine = dsm + warp * outs;
-  for (uint64_t n64 = F0 / U; n64 * U < F1; ++n64) {
-    const uint32_t n = (uint32_t)n64;
-    const uint64_t tb = n64 * U, te = tb + U;
-    const uint32_t lo = (uint32_t)(max(F0, tb) - tb), len = (uint32_t)(min(F1, te) - tb) - lo;
-    const uint32_t f0 = lo + (uint32_t)((uint64_t)len * warp / EWARPS), f1 = lo + (uint32_t)((uint64_t)len * (warp + 1) / EWARPS);
-    for (uint32_t i = lane; i < outs; i += 32) mine[i] = 0.f;
+  const bool whole_tiles = U <= 6 * EWARPS;
+  const uint32_t parts = (uint32_t)min((uint64_t)gridDim.x, whole_tiles ? (uint64_t)ntile : (total + EWARPS - 1) / EWARPS);
+  // Part b: units [bound(b), bound(b + 1)) of the flat sequence, whole tiles if `whole_tiles`.
+  const uint64_t items = whole_tiles ? (uint64_t)ntile : total, share_q = quotient(items, parts), share_r = items - share_q * parts;
+  auto bound = [&](uint32_t b) { return (b * share_q + min((uint64_t)b, share_r)) * (whole_tiles ? U : 1u); };
+  const bool works = blockIdx.x < parts;
+  const uint64_t F0 = works ? bound(blockIdx.x) : 0, F1 = works ? bound(blockIdx.x + 1) : 0;
+  const uint32_t n0 = works ? (uint32_t)quotient(F0, U) : 1u, n1 = works ? (uint32_t)quotient(F1 - 1, U) : 0u;
+  // This warp's share [lo, hi) of the units of tile n that belong to this CTA.
+  auto share = [&](uint32_t n, uint32_t& lo, uint32_t& hi) {
+    const uint64_t tb = (uint64_t)n * U;
+    const uint32_t from = (uint32_t)(max(F0, tb) - tb), len = (uint32_t)(min(F1, tb + U) - tb) - from;
+    lo = from + (uint32_t)((uint64_t)len * warp / EWARPS);
+    hi = from + (uint32_t)((uint64_t)len * (warp + 1) / EWARPS);
+  };
+  uint32_t rn = n0, rseg = 0, rleft = 0, rem = 0, lo = 0, hi = 0;      // the units being requested
+  auto request_from = [&](uint32_t a, uint32_t b) {
+    rem = b - a;
+    rseg = a / Gi;
+    rleft = Gi - (a - rseg * Gi);
+    if (rem > 0) ring.locate(p.d_codes, p.d_scales, ((size_t)pl.seg_e[rseg] * ntile + rn) * Gi + (Gi - rleft));
+  };
+  auto fill = [&]() {
+    while (rem == 0 && rn < n1) {                                      // on to the next tile's share
+      uint32_t a, b;
+      share(++rn, a, b);
+      request_from(a, b);
+    }
+    if (rem > 0) {
+      ring.copy();
+      --rem;
+      if (--rleft == 0 && rem > 0) {
+        rleft = Gi;
+        ring.locate(p.d_codes, p.d_scales, ((size_t)pl.seg_e[++rseg] * ntile + rn) * Gi);
+      }
+    }
+    cp_commit();
+    ring.step();
+  };
+  ring.init(esm, warp, lane);
+  if (works) {                                                         // the first weights do not wait for h
+    share(n0, lo, hi);
+    request_from(lo, hi);
+#pragma unroll 1
+    for (int i = 0; i < RING; ++i) fill();
+  }
+  constexpr int OUTS = kMaxTokens * 32 / ETHREADS;                     // outputs of a tile per thread
+  float* sums = reinterpret_cast<float*>(esm + RING_BYTES);            // [EWARPS][T][32]
+  float* rows = sums + warp * outs;
+  // The residual of this thread's outputs of tile n, where this CTA finishes it alone.
+  auto residual_of = [&](uint32_t n, float (&r)[OUTS]) {
+#pragma unroll
+    for (int k = 0; k < OUTS; ++k) {
+      const uint32_t i = threadIdx.x + k * ETHREADS;
+      r[k] = p.residual && i < outs ? __bfloat162float(p.residual[(size_t)(i / 32) * H + n * 32 + i % 32]) : 0.f;
+    }
+  };
+  auto clear_rows = [&]() {
+    for (uint32_t i = lane; i < outs; i += 32) rows[i] = 0.f;
+  };
+  float res[OUTS] = {};
+  if (works) {
+    clear_rows();
+    if (F0 <= (uint64_t)n0 * U && F1 >= (uint64_t)n0 * U + U) residual_of(n0, res);
+  }
+  grid.barrier_wait(std::move(arrived));
+
+  const __nv_bfloat16* h = p.h;
+  if (p.stage) {                                                       // all of h fits behind the rows
+    float* to = sums + EWARPS * outs;
+    if (works)
+      for (uint32_t i = threadIdx.x * 16; i < low * 4; i += ETHREADS * 16)
+        cp_async16(smem_addr(to) + i, reinterpret_cast<const uint8_t*>(p.h) + i);
+    cp_commit();
+    cp_wait<0>();
+    __syncthreads();
+    h = reinterpret_cast<const __nv_bfloat16*>(to);
+  }
+  // The parts with a unit of tile n: b0 .. b1.  The first share_r parts hold one item more.
+  auto owner = [&](uint64_t u) {
+    const uint64_t wide = share_r * (share_q + 1);
+    return (uint32_t)(u < wide ? quotient(u, share_q + 1) : share_r + quotient(u - wide, share_q));
+  };
+  for (uint32_t n = n0; n <= n1; ++n) {
+    const uint64_t tb = (uint64_t)n * U;
+    const bool whole = F0 <= tb && F1 >= tb + U;
+    if (n > n0) {
+      clear_rows();
+      if (whole) residual_of(n, res);
+    }
     __syncwarp();
-    if (f0 < f1) {
-      uint32_t seg = f0 / Gi, g = f0 % Gi, nseg = seg, ng = g;
-      size_t nunit = 0;
-      auto locate = [&]() { nunit = ((size_t)pl.seg_e[nseg] * ntile + n) * Gi + ng; };
-      auto advance = [&]() {
-        ++nunit;
-        if (++ng == Gi) {
-          ng = 0;
-          if (++nseg < pl.segments) locate();
-        }
+    share(n, lo, hi);
+    if (lo < hi) {
+      // Columns 0 .. 3 of an MMA tile are the high halves of four tokens' h, columns 4 .. 7
+      // the low halves.  A segment of up to four tokens needs one MMA tile: its next unit's
+      // h is requested a unit ahead.
+      uint32_t seg = lo / Gi, g = lo - seg * Gi, left = hi - lo, m = 0;
+      const __nv_bfloat16* row[2] = {nullptr, nullptr};
+      uint4 hv[2][4];
+      auto load_h = [&](uint4 (&d)[4], int t, uint32_t at) {
+        const uint4* q = reinterpret_cast<const uint4*>(row[t]) + at * 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = q[4 * i];
       };
-      locate();
-      Weights wa, wb;
-      load_unit(wa, p.d_codes, p.d_scales, nunit, lane);
-      advance();
-      const uint4 *hi = nullptr, *lw = nullptr;
-      auto row_of = [&](uint32_t s) {
-        hi = lw = nullptr;
-        if (g8 < pl.seg_n[s]) {
-          const size_t at = (size_t)pl.pair[pl.seg_s[s] + g8] * p.I + 32 * c;
-          hi = reinterpret_cast<const uint4*>(p.h_hi + at);
-          lw = reinterpret_cast<const uint4*>(p.h_lo + at);
+      auto begin = [&]() {                                             // segment seg: its rows, the first unit's h
+        const uint32_t s0 = pl.seg_s[seg];
+        m = pl.seg_n[seg];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t col = 4 * t + (g8 & 3u);
+          row[t] = h + (g8 >> 2) * low + (size_t)pl.pair[s0 + (col < m ? col : 0)] * I + 8 * c;
         }
+        load_h(hv[0], 0, g);
+        if (m > 4) load_h(hv[1], 1, g);
       };
-      row_of(seg);
-      float acc[2][4] = {};
-      for (uint32_t f = f0; f < f1; ++f) {
-        if (f + 1 < f1) {
-          load_unit(wb, p.d_codes, p.d_scales, nunit, lane);
-          advance();
-        }
-        uint4 b[2][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          b[0][i] = hi ? hi[g * 16 + i] : make_uint4(0, 0, 0, 0);
-          b[1][i] = hi ? lw[g * 16 + i] : make_uint4(0, 0, 0, 0);
-        }
-        float d[2][4];
-        unit_products<2>(wa, b, d);
-        add_scaled(acc, d, wa.s);
-        wa = wb;
-        if (++g == Gi || f + 1 == f1) {                            // this segment's share is complete
-          const uint32_t m = pl.seg_n[seg], s = pl.seg_s[seg];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t col = 2 * c + k;
-            if (col < m) {
-              float* r = mine + (pl.pair[s + col] / p.topk) * 32 + g8;
-#pragma unroll
-              for (int tt = 0; tt < 2; ++tt) {
-                r[16 * tt] += acc[tt][k];
-                r[16 * tt + 8] += acc[tt][2 + k];
-              }
+      begin();
+      while (left > 0) {
+        const uint32_t run = min(Gi - g, left), s0 = pl.seg_s[seg], tokens = m;
+        float acc[2][2][4] = {};                                       // [MMA tile][16-row tile]
+        const float none1[1][2] = {}, none2[2][2] = {};
+        Weights w;
+        auto next = [&]() {
+          cp_wait<RING - 1>();
+          w.read(ring.at, lane);
+        };
+        if (tokens <= 4) {
+          auto one = [&](int t) {
+            next();
+            unit_products<false, 1>(w, reinterpret_cast<const uint4 (&)[1][4]>(hv[t]), none1, reinterpret_cast<float (&)[1][2][4]>(acc[0]));
+            fill();
+          };
+          for (uint32_t k = 0; k < run; k += 2) {
+            if (k + 1 < run) load_h(hv[1], 0, g + k + 1);
+            one(0);
+            if (k + 1 < run) {
+              if (k + 2 < run) load_h(hv[0], 0, g + k + 2);
+              one(1);
             }
           }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[0][i] = acc[1][i] = 0.f;
-          if (g == Gi) {
-            g = 0;
-            if (++seg < pl.segments) row_of(seg);
+        } else {
+          for (uint32_t k = 0; k < run; ++k) {
+            next();
+            unit_products<false, 2>(w, hv, none2, acc);
+            if (k + 1 < run) {
+              load_h(hv[0], 0, g + k + 1);
+              load_h(hv[1], 1, g + k + 1);
+            }
+            fill();
           }
         }
+        left -= run;
+        g = 0;
+        ++seg;
+        if (left > 0) begin();
+        // The segment's sums per token: high plus low columns, a 16-row tile by each half of the lanes.
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (t == 0 || tokens > 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float v0 = acc[t][0][i] + __shfl_xor_sync(0xFFFFFFFFu, acc[t][0][i], 2);
+              const float v1 = acc[t][1][i] + __shfl_xor_sync(0xFFFFFFFFu, acc[t][1][i], 2);
+              const uint32_t col = 4 * t + 2 * (c & 1u) + (i & 1);
+              if (col < tokens) rows[pl.token[s0 + col] * 32 + g8 + ((i & 2) ? 8 : 0) + (c < 2 ? 0 : 16)] += c < 2 ? v0 : v1;
+            }
+          }
+        __syncwarp();
       }
     }
     __syncthreads();
-    const bool whole = F0 <= tb && F1 >= te;
     auto warps_sum = [&](uint32_t i) {
       float s = 0.f;
 #pragma unroll
-      for (uint32_t w = 0; w < EWARPS; ++w) s += dsm[w * outs + i];
+      for (uint32_t w = 0; w < EWARPS; ++w) s += sums[w * outs + i];
       return s;
     };
-    auto put = [&](uint32_t i, float v) {
-      const size_t at = (size_t)(i / 32) * p.H + n * 32 + i % 32;
-      if (p.residual) v += __bfloat162float(p.residual[at]);
-      p.y[at] = __float2bfloat16_rn(v);
-    };
     if (whole) {
-      for (uint32_t i = threadIdx.x; i < outs; i += ETHREADS) put(i, warps_sum(i));
+#pragma unroll
+      for (int k = 0; k < OUTS; ++k) {
+        const uint32_t i = threadIdx.x + k * ETHREADS;
+        if (i < outs) p.y[(size_t)(i / 32) * H + n * 32 + i % 32] = __float2bfloat16_rn(warps_sum(i) + res[k]);
+      }
+      __syncthreads();                                                 // the rows are cleared for the next tile
     } else {
       // Part b's slot for this tile: 0 if the tile is the first of its range, else 1.
       float* to = p.partial + ((size_t)2 * blockIdx.x + (F0 >= tb ? 0 : 1)) * outs;
       for (uint32_t i = threadIdx.x; i < outs; i += ETHREADS) __stcg(to + i, warps_sum(i));
-      const uint32_t b0 = (uint32_t)(((tb + 1) * parts - 1) / total), b1 = (uint32_t)((te * parts - 1) / total);
-      __threadfence();
       __syncthreads();
-      if (threadIdx.x == 0) last = atomicAdd(p.tickets + n, 1u) == b1 - b0 ? 1u : 0u;
-      __syncthreads();
-      if (last) {
-        __threadfence();
-        for (uint32_t i = threadIdx.x; i < outs; i += ETHREADS) {
-          float s = 0.f;
-          for (uint32_t b = b0; b <= b1; ++b)
-            s += __ldcg(p.partial + ((size_t)2 * b + (total * b / parts >= tb ? 0 : 1)) * outs + i);
-          put(i, s);
-        }
+      if (threadIdx.x == 0) last[n == n0 ? 0 : 1] = ticket(p.tickets + n) == owner(tb + U - 1) - owner(tb) ? 1u : 0u;
+    }
+  }
+  __syncthreads();
+  // The cut tiles (the first and the last of the range at most) for which this CTA came last.
+  for (uint32_t k = 0; k < 2; ++k) {
+    const uint32_t n = k ? n1 : n0;
+    const uint64_t tb = (uint64_t)n * U;
+    if (!works || (k == 1 && n1 == n0) || (F0 <= tb && F1 >= tb + U) || !last[k]) continue;
+    const uint32_t b0 = owner(tb), count = owner(tb + U - 1) - b0 + 1;
+    const float* from = p.partial + ((size_t)2 * b0 + (bound(b0) >= tb ? 0 : 1)) * outs;   // later parts begin with this tile
+    residual_of(n, res);
+#pragma unroll
+    for (int j = 0; j < OUTS; ++j) {
+      const uint32_t i = threadIdx.x + j * ETHREADS;
+      if (i < outs) {
+        float s = __ldcg(from + i);
+#pragma unroll 4
+        for (uint32_t b = 1; b < count; ++b) s += __ldcg(p.partial + (size_t)2 * (b0 + b) * outs + i);
+        p.y[(size_t)(i / 32) * H + n * 32 + i % 32] = __float2bfloat16_rn(s + res[j]);
       }
     }
-    __syncthreads();                                               // the rows are zeroed for the next tile
   }
 }
 

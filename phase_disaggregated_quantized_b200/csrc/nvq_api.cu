@@ -592,12 +592,12 @@ nvq_status nvfp4_gemm_w4a4_epilogue(const uint8_t* x_codes, const uint8_t* x_sca
     return fail(NVQ_ERR_UNSUPPORTED_SHAPE, "nvfp4_gemm_w4a4_epilogue: need N % 8 == 0, K % 64 == 0");
   if (M >= kMaxDim || N >= kMaxDim || K >= kMaxDim || !gemm_tiles_fit(M, N))
     return fail(NVQ_ERR_UNSUPPORTED_SHAPE, "nvfp4_gemm_w4a4_epilogue: too large");
+  if (M == 0) return NVQ_OK;
   if (!x_codes || !x_scales || !t_x || !w_codes || !w_scales || !t_w || !y_bf16)
     return fail(NVQ_ERR_INVALID_ARG, "nvfp4_gemm_w4a4_epilogue: NULL pointer");
   if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) ||
       !aligned16(y_bf16) || (reinterpret_cast<uintptr_t>(t_x) & 3u) || (reinterpret_cast<uintptr_t>(t_w) & 3u))
     return fail(NVQ_ERR_MISALIGNED, "nvfp4_gemm_w4a4_epilogue: pointer not aligned");
-  if (M == 0) return NVQ_OK;
   nvq::EpiParams ep;
   const nvq_status st = epilogue_params("nvfp4_gemm_w4a4_epilogue", epilogue, y_bf16, M, N, &ep);
   if (st != NVQ_OK) return st;
@@ -737,35 +737,38 @@ nvq_status w4a16_sparse24_gemm(const void* x_bf16, const uint8_t* packed, const 
 // ------------------------------------------------------------------ mixture of experts
 namespace {
 
-// CTAs of the expert kernels: two on each of a B200's SMs.  A constant, so that
-// the workspace (one partial tile pair per CTA of the down kernel) can be sized without a device.
-constexpr int kMoeMaxGrid = 2 * 148;
+// CTAs of the expert kernel: one on each of a B200's SMs.  A constant, so that the
+// workspace (two partial tiles per CTA) can be sized without a device.
+constexpr int kMoeMaxGrid = 148;
 constexpr int64_t kMoeMaxDim = (int64_t)1 << 20;   // H and I: a CTA's unit counts stay in 32 bits
 
 struct MoeWs {
-  size_t hi, lo, tickets, partial, total;
+  size_t h, tickets, partial, logits, total;
 };
 MoeWs moe_ws_layout(int64_t T, int64_t H, int64_t I, int64_t topk) {
   const size_t tc = (size_t)std::min<int64_t>(T, nvq::moe::kMaxTokens);
-  const size_t half = align256(tc * (size_t)topk * (size_t)I * 2);
   MoeWs W;
-  W.hi = 0;
-  W.lo = half;
-  W.tickets = 2 * half;
+  W.h = 0;
+  W.tickets = align256(tc * (size_t)topk * (size_t)I * 4);
   W.partial = W.tickets + align256((size_t)(H / 32) * 4);
-  W.total = W.partial + (size_t)2 * kMoeMaxGrid * tc * 32 * 4;
+  W.logits = W.partial + align256((size_t)2 * kMoeMaxGrid * tc * 32 * 4);
+  W.total = W.logits + (size_t)kMoeMaxGrid * 16 * tc * 4;   // at most one 16-expert tile per CTA
   return W;
 }
 
-// Once per device and kernel: the shared-memory opt-in.
+// Once per device and kernel: the opt-ins to more shared memory and to clusters of more than 8 CTAs.
 template <typename K>
-nvq_status smem_opt_in(K kernel, int bytes, std::once_flag (&once)[kMaxDevices], cudaError_t (&err)[kMaxDevices],
-                       const char* where) {
+nvq_status kernel_opt_in(K kernel, int bytes, bool wide_cluster, std::once_flag (&once)[kMaxDevices],
+                         cudaError_t (&err)[kMaxDevices], const char* where) {
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, where);
   if (dev < 0 || dev >= kMaxDevices) return fail(NVQ_ERR_CUDA, "device index out of range");
-  std::call_once(once[dev], [&] { err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+  std::call_once(once[dev], [&] {
+    err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err[dev] == cudaSuccess && wide_cluster)
+      err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
   return err[dev] == cudaSuccess ? NVQ_OK : cuda_fail(err[dev], where);
 }
 
@@ -844,7 +847,7 @@ nvq_status launch_route(const void* x, const void* wr, int64_t T, int64_t E, int
   using namespace nvq::moe;
   static std::once_flag once[kMaxDevices];
   static cudaError_t err[kMaxDevices];
-  const nvq_status st = smem_opt_in(route_kernel, RouteShape(kMaxExperts).smem(), once, err, "moe_route: smem attribute");
+  const nvq_status st = kernel_opt_in(route_kernel, RouteShape::max_smem(), RCS > 8, once, err, "moe_route: kernel attributes");
   if (st != NVQ_OK) return st;
   const int64_t clusters = (T + kMaxTokens - 1) / kMaxTokens;
   return launch_dependent("route_kernel", route_kernel, (int)(clusters * RCS), RTHREADS, RouteShape((int)E).smem(), RCS,
@@ -852,32 +855,53 @@ nvq_status launch_route(const void* x, const void* wr, int64_t T, int64_t E, int
                           (uint32_t)T, (uint32_t)E, (uint32_t)H, (uint32_t)topk, renorm ? 1u : 0u, ids, weights);
 }
 
-// 32 tokens at a time: gate and up, then down.
+// 32 tokens at a time, one cooperative launch each.
+template <bool ROUTE>
 nvq_status launch_experts(nvq::moe::ExpertParams p, int64_t T, void* workspace, cudaStream_t stream) {
   using namespace nvq::moe;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t err[kMaxDevices];
+  const nvq_status st = kernel_opt_in(moe_kernel<ROUTE>, RING_BYTES + kBehindRing, false, once, err, "w4a16_moe: kernel attributes");
+  if (st != NVQ_OK) return st;
   const MoeWs W = moe_ws_layout(T, p.H, p.I, p.topk);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  p.h_hi = reinterpret_cast<__nv_bfloat16*>(ws + W.hi);
-  p.h_lo = reinterpret_cast<__nv_bfloat16*>(ws + W.lo);
+  p.h = reinterpret_cast<__nv_bfloat16*>(ws + W.h);
   p.tickets = reinterpret_cast<uint32_t*>(ws + W.tickets);
   p.partial = reinterpret_cast<float*>(ws + W.partial);
-  const int grid = std::min(kMoeMaxGrid, 2 * sm_count());
+  p.logits = reinterpret_cast<float*>(ws + W.logits);
+  const int grid = std::min(kMoeMaxGrid, sm_count());
+  p.by_topk = FastDiv(p.topk);
+  p.by_grid = FastDiv((uint32_t)grid);
+  p.by_g = FastDiv(p.H / 128);
+  p.by_rtiles = FastDiv(p.I / 16);
+  p.etiles = (p.E + 15) / 16;
+  // Slices of K of the router: no more (tile, slice) pairs than CTAs, a 64-wide block of K for each warp.
+  p.slices = std::max(1u, std::min((uint32_t)grid / p.etiles, p.H / 64 / EWARPS));
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(ETHREADS, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   for (int64_t t0 = 0; t0 < T; t0 += kMaxTokens) {
     p.T = (uint32_t)std::min<int64_t>(kMaxTokens, T - t0);
-    nvq_status st = launch_dependent("gate_up_kernel", gate_up_kernel, grid, ETHREADS, 0, 0, stream, p);
-    if (st == NVQ_OK)
-      st = launch_dependent("down_kernel", down_kernel, grid, ETHREADS, (size_t)EWARPS * p.T * 32 * 4, 0, stream, p);
-    if (st != NVQ_OK) return st;
+    p.stage = stage_h(p.T, p.T * p.topk, p.I) ? 1u : 0u;
+    cfg.dynamicSmemBytes = (size_t)layer_smem(p.T, p.T * p.topk, p.I);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_kernel<ROUTE>, p);
+    if (e != cudaSuccess) return cuda_fail(e, "moe_kernel launch");
     p.x += (size_t)p.T * p.H;
     p.y += (size_t)p.T * p.H;
     if (p.residual) p.residual += (size_t)p.T * p.H;
     p.ids += (size_t)p.T * p.topk;
     p.weights += (size_t)p.T * p.topk;
   }
-  return NVQ_OK;
+  return launch_status("moe_kernel");
 }
 
-nvq::moe::ExpertParams expert_params(const void* x, const int32_t* ids, const float* weights,
+nvq::moe::ExpertParams expert_params(const void* x, int32_t* ids, float* weights,
                                      const void* const (&packed)[4], const void* residual, void* y, int64_t E,
                                      int64_t H, int64_t I, int topk) {
   nvq::moe::ExpertParams p = {};
@@ -922,8 +946,9 @@ nvq_status w4a16_moe_experts(const void* x_bf16, const int32_t* ids, const float
   const nvq_status st = experts_validate("w4a16_moe_experts", x_bf16, ids, weights, packed, residual_bf16, y_bf16, T, E,
                                          H, I, topk, workspace, workspace_bytes);
   if (st != NVQ_OK || T == 0) return st;
-  return launch_experts(expert_params(x_bf16, ids, weights, packed, residual_bf16, y_bf16, E, H, I, topk), T, workspace,
-                        static_cast<cudaStream_t>(stream));
+  return launch_experts<false>(expert_params(x_bf16, const_cast<int32_t*>(ids), const_cast<float*>(weights), packed,
+                                             residual_bf16, y_bf16, E, H, I, topk),
+                               T, workspace, static_cast<cudaStream_t>(stream));
 }
 
 nvq_status w4a16_moe(const void* x_bf16, const void* w_router_bf16, const uint8_t* gate_up_codes,
@@ -938,10 +963,10 @@ nvq_status w4a16_moe(const void* x_bf16, const void* w_router_bf16, const uint8_
   st = experts_validate("w4a16_moe", x_bf16, ids, weights, packed, residual_bf16, y_bf16, T, E, H, I, topk, workspace,
                         workspace_bytes);
   if (st != NVQ_OK || T == 0) return st;
-  st = launch_route(x_bf16, w_router_bf16, T, E, H, topk, renormalize != 0, ids, weights, stream);
-  if (st != NVQ_OK) return st;
-  return launch_experts(expert_params(x_bf16, ids, weights, packed, residual_bf16, y_bf16, E, H, I, topk), T, workspace,
-                        stream);
+  nvq::moe::ExpertParams p = expert_params(x_bf16, ids, weights, packed, residual_bf16, y_bf16, E, H, I, topk);
+  p.wr = static_cast<const __nv_bfloat16*>(w_router_bf16);
+  p.renorm = renormalize != 0 ? 1u : 0u;
+  return launch_experts<true>(p, T, workspace, stream);
 }
 
 // ------------------------------------------------------------------ phase dispatch

@@ -133,39 +133,41 @@ def test_interleave_in_blocks_of_16():
     assert w == [*range(16), *range(100, 116), *range(16, 32), *range(116, 132)]
 
 
-# ------------------------------------------------------------------ mirrors of the kernels' index arithmetic
-WARPS, COLS = 8, 8
+# ------------------------------------------------------------------ mirrors of the kernel's index arithmetic
+WARPS, COLS, GRID, UNIT_COST = 16, 8, 148, 28
 
 
 def plan(ids, E):
-    """(segments as (expert, first slot, tokens), slot -> pair) as the kernels build them, by masks."""
+    """(segments as (expert, first slot, tokens), slot -> pair) as the kernel builds them: up to 32
+    pairs by one warp, experts in the order of their first pair; else by token masks, in expert order."""
     T, topk = ids.shape
-    first = [[0 <= ids[t, j] < E and ids[t, j] not in ids[t, :j] for j in range(topk)] for t in range(T)]
-    mask = [0] * E
-    for t in range(T):
-        for j in range(topk):
-            if first[t][j]:
-                mask[ids[t, j]] |= 1 << t
-    segs, start, slot = [], {}, 0
-    for e in range(E):
-        n = bin(mask[e]).count("1")
-        start[e] = slot
-        segs += [(e, slot + q, min(COLS, n - q)) for q in range(0, n, COLS)]
-        slot += n
-    pair = [None] * slot
-    for t in range(T):
-        for j in range(topk):
-            if first[t][j]:
-                e = ids[t, j]
-                pair[start[e] + bin(mask[e] & ((1 << t) - 1)).count("1")] = t * topk + j
+    flat = [int(v) for v in ids.ravel()]
+    first = [0 <= v < E and v not in flat[i // topk * topk:i] for i, v in enumerate(flat)]
+    if T * topk <= 32:
+        order = []
+        for i, v in enumerate(flat):
+            if first[i] and v not in order:
+                order.append(v)
+    else:
+        order = range(E)
+    segs, pair = [], []
+    for e in order:
+        mine = [i for i, v in enumerate(flat) if first[i] and v == e]         # by token: the rank is a count of mask bits
+        segs += [(e, len(pair) + q, min(COLS, len(mine) - q)) for q in range(0, len(mine), COLS)]
+        pair += mine
     return segs, pair
+
+
+def _random_ids(rng):
+    T, topk, E = int(rng.integers(1, 33)), int(rng.integers(1, 17)), int(rng.integers(1, 40))
+    return rng.integers(-2, E + 2, size=(T, topk)), E
 
 
 def test_plan_holds_every_choice_once():
     rng = np.random.default_rng(1)
     for _ in range(300):
-        T, topk, E = int(rng.integers(1, 33)), int(rng.integers(1, 17)), int(rng.integers(1, 40))
-        ids = rng.integers(-2, E + 2, size=(T, topk))
+        ids, E = _random_ids(rng)
+        T, topk = ids.shape
         segs, pair = plan(ids, E)
         want = sorted({(int(ids[t, j]), t) for t in range(T) for j in range(topk) if 0 <= ids[t, j] < E})
         got = []
@@ -176,73 +178,150 @@ def test_plan_holds_every_choice_once():
             got += [(e, t) for t in toks]
         assert sorted(got) == want
         assert len(segs) <= T * topk
+        assert [s for _, s, _ in segs] == [sum(n for _, _, n in segs[:i]) for i in range(len(segs))]
+
+
+def fast_div(d):
+    """The kernel's n / d for n < 2^31."""
+    l = 0
+    while l < 31 and (1 << l) < d:
+        l += 1
+    mul, shift = ((1 << (31 + l)) + d - 1) // d, 31 + l
+    assert mul < 1 << 32
+    return lambda n: (n * mul) >> shift
+
+
+def test_fast_division_is_exact():
+    rng = random.Random(4)
+    for d in [*range(1, 300), 1 << 16, (1 << 16) + 1, (1 << 20) - 1, 65535, 8192]:
+        f = fast_div(d)
+        tops = [(1 << 31) - 1, ((1 << 31) - 1) // d * d, ((1 << 31) - 1) // d * d - 1]
+        for n in tops + [0, 1, d - 1, d, d + 1] + [rng.randrange(1 << 31) for _ in range(50)]:
+            if n >= 0:
+                assert f(n) == n // d
 
 
 def cut(n, w, parts):
     return n * w // parts
 
 
+def first_tile(segs, rtiles, grid, b):
+    slots = segs[-1][1] + segs[-1][2] if segs else 0
+    cost = (UNIT_COST * len(segs) + slots) * rtiles
+    quot, rest = cost // grid, cost % grid
+    at = b * quot + min(b, rest)
+    s = sum((UNIT_COST * k + seg[1]) * rtiles <= at for k, seg in enumerate(segs))
+    if s == 0 or at == cost:
+        return len(segs) * rtiles
+    s -= 1
+    return s * rtiles + (at - (UNIT_COST * s + segs[s][1]) * rtiles) // (UNIT_COST + segs[s][2])
+
+
 def test_gate_up_split_covers_every_unit_once():
-    rng = random.Random(2)
-    for _ in range(400):
-        grid, tiles, G = rng.choice([1, 7, 296]), rng.choice([0, 1, 3, 50, 400, 5000]), rng.choice([1, 2, 9, 16, 40])
-        for b in rng.sample(range(grid), min(grid, 8)):
-            T0, T1 = cut(tiles, b, grid), cut(tiles, b + 1, grid)
-            length = (T1 - T0) * G
+    rng, nrng = random.Random(2), np.random.default_rng(2)
+    for _ in range(150):
+        ids, E = _random_ids(nrng)
+        segs, _ = plan(ids, E)
+        rtiles, G, grid = rng.choice([8, 16, 40, 88]), rng.choice([1, 2, 9, 16, 40]), rng.choice([1, 7, GRID])
+        bounds = [first_tile(segs, rtiles, grid, b) for b in range(grid + 1)]
+        assert bounds == sorted(bounds) and bounds[-1] == len(segs) * rtiles and (not segs or bounds[0] == 0)
+        for b in rng.sample(range(grid), min(grid, 6)):
+            mine = bounds[b + 1] - bounds[b]
+            length = mine * G
             direct, slots = set(), {}
             for w in range(WARPS):
                 f0, f1 = cut(length, w, WARPS), cut(length, w + 1, WARPS)
                 if f0 == f1:
                     continue
                 tile, g, start = f0 // G, f0 % G, f0
+                head = g != 0
                 for f in range(f0, f1):
                     g += 1
                     if g == G:
-                        if f0 % G and tile == f0 // G:
+                        if head:
                             slots[w, 0] = (tile, start, f + 1)
                         else:
                             direct.add(tile)
-                            assert start == tile * G and f + 1 == start + G
-                        g, tile, start = 0, tile + 1, f + 1
+                            assert start == tile * G
+                        head, g, tile, start = False, 0, tile + 1, f + 1
                 if g:
-                    slots[w, 0 if tile == f0 // G else 1] = (tile, start, f1)
-            for i in range(T1 - T0):
-                tb, te = i * G, (i + 1) * G
-                at = tb
-                for w in range(WARPS):
-                    a, e = cut(length, w, WARPS), cut(length, w + 1, WARPS)
-                    if a < e and a < te and e > tb and not (a <= tb and e >= te):
-                        tile, s0, s1 = slots.pop((w, 0 if a >= tb else 1))
-                        assert tile == i and s0 == at
-                        at = s1
-                assert at in (tb, te) and (i in direct) == (at == tb)
-            assert not slots
+                    slots[w, 0 if f0 // G == (f1 - 1) // G else 1] = (tile, start, f1)
+            finished = set()
+            for w in range(1, WARPS):
+                f0 = cut(length, w, WARPS)
+                tb = f0 // G * G
+                te = tb + G
+                if f0 != tb and f0 < length and cut(length, w - 1, WARPS) <= tb:
+                    at, k = tb, w - 1
+                    while k < WARPS and cut(length, k, WARPS) < te:
+                        a = cut(length, k, WARPS)
+                        if a != cut(length, k + 1, WARPS):
+                            tile, s0, s1 = slots.pop((k, 0 if a >= tb else 1))
+                            assert tile == tb // G and s0 == at
+                            at = s1
+                        k += 1
+                    assert at == te
+                    finished.add(tb // G)
+            assert not slots and finished | direct == set(range(mine)) and not finished & direct
 
 
 def test_down_split_covers_every_unit_once_and_finds_every_part():
     rng = random.Random(3)
-    for _ in range(400):
-        grid, tiles, U = rng.choice([2, 296]), rng.choice([4, 8, 64, 160]), rng.choice([1, 2, 3, 12, 48, 672])
-        total = tiles * U
-        parts = min(grid, -(-total // WARPS))
-        seen, count, slot_of = 0, {}, {}
+    for _ in range(500):
+        grid, tiles, U = rng.choice([2, GRID]), rng.choice([4, 8, 64, 128, 160]), rng.choice([1, 2, 3, 12, 48, 96, 97, 672])
+        total, whole_tiles = tiles * U, U <= 6 * WARPS
+        parts = min(grid, tiles if whole_tiles else -(-total // WARPS))
+        items = tiles if whole_tiles else total
+        q, r = divmod(items, parts)
+        bound = lambda b: (b * q + min(b, r)) * (U if whole_tiles else 1)                # noqa: E731
+        owner = lambda u: u // (q + 1) if u < r * (q + 1) else r + (u - r * (q + 1)) // q   # noqa: E731
+        count, slot_of, whole = {}, {}, set()
         for b in range(parts):
-            F0, F1 = total * b // parts, total * (b + 1) // parts
-            assert F0 == seen and F1 > F0
-            seen = F1
-            n = F0 // U
-            while n * U < F1:
-                tb, te = n * U, n * U + U
-                if not (F0 <= tb and F1 >= te):
+            F0, F1 = bound(b), bound(b + 1)
+            assert F1 > F0 and (b > 0 or F0 == 0)
+            n0, n1, cut_tiles = F0 // U, (F1 - 1) // U, []
+            for n in range(n0, n1 + 1):
+                tb = n * U
+                if F0 <= tb and F1 >= tb + U:
+                    assert n not in whole
+                    whole.add(n)
+                else:
+                    cut_tiles.append(n)
                     count[n] = count.get(n, 0) + 1
                     s = 2 * b + (0 if F0 >= tb else 1)
                     assert s not in slot_of                   # a slot holds one tile's part
                     slot_of[s] = n
-                n += 1
-        assert seen == total
+                lo = max(F0, tb) - tb
+                size = min(F1, tb + U) - tb - lo
+                at = lo
+                for w in range(WARPS):                        # the warps' shares follow one another
+                    assert lo + size * w // WARPS == at
+                    at = lo + size * (w + 1) // WARPS
+                assert at == lo + size
+            assert set(cut_tiles) <= {n0, n1} and not (whole_tiles and cut_tiles)
+        assert bound(parts) == total
+        assert whole | set(count) == set(range(tiles)) and not whole & set(count)
         for n, c in count.items():
-            tb, te = n * U, n * U + U
-            b0, b1 = ((tb + 1) * parts - 1) // total, (te * parts - 1) // total
+            tb = n * U
+            b0, b1 = owner(tb), owner(tb + U - 1)
             assert b1 - b0 + 1 == c
             for b in range(b0, b1 + 1):
-                assert slot_of[2 * b + (0 if total * b // parts >= tb else 1)] == n
+                s = 2 * b + ((0 if bound(b0) >= tb else 1) if b == b0 else 0)
+                assert slot_of[s] == n
+
+
+def h_at(column):
+    """Where the kernel keeps a column of h: by row tile and row, as gate and up write it."""
+    rt, row = divmod(column, 16)
+    k = (rt & 7) * 16
+    return (rt >> 3) * 128 + (k & 16) * 4 + (k >> 5) * 8 + (row & 7) + 32 * (row >> 3)
+
+
+def test_order_of_h_is_the_one_that_down_reads():
+    at = [h_at(k) for k in range(512)]
+    assert sorted(at) == list(range(512))
+    for grp in range(4):
+        for c in range(4):
+            for i in range(4):
+                for e in range(8):                            # lane c's i-th load: 8 values from 32 i + 8 c on
+                    assert at[grp * 128 + 32 * c + 8 * i + e] == grp * 128 + 32 * i + 8 * c + e
