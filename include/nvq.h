@@ -456,7 +456,8 @@ nvq_status nvq_linear_epilogue(const void* x_bf16, int64_t M, int64_t N, int64_t
  * Launched with programmatic dependent launch under the rules of w4a16_gemm
  * (packed weights constant, all else after the wait on the preceding kernel).
  * Shape rules: T >= 0, 1 <= E <= 512, 1 <= topk <= 16; router: topk <= E,
- * H % 64 == 0; experts: H % 128 == 0, I % 128 == 0, both < 2^20.  Pointers
+ * H % 64 == 0; experts: H % 128 == 0, I % 128 == 0, both < 2^20, H * I < 2^33.
+ * Pointers
  * 16-byte aligned, ids and weights 4.
  * ------------------------------------------------------------------------ */
 nvq_status moe_route(const void* x_bf16, const void* w_router_bf16, int64_t T, int64_t E, int64_t H, int topk,

@@ -386,49 +386,42 @@ def nvq_linear(x, w4a4=None, w4a16=None, N: int | None = None, *, crossover_m: i
 
 
 # ------------------------------------------------------------------ products with an epilogue
-# These calls are a few microseconds on the GPU, so the binding looks at each
+# These calls take a few microseconds on the GPU, so the binding looks at each
 # tensor once and takes the stream's handle without making a stream object.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
 def _elsewhere(idx, stream):
     """None if a call on tensors of device idx can be made as things are: the device is current and
     no stream is named.  Else the context to make it in (what it allocates then belongs to that stream)."""
+    if idx < 0:
+        raise ValueError("libnvq calls take CUDA tensors")
     if stream is None:
-        return None if idx == torch.cuda.current_device() else torch.cuda.device(idx)
+        return None if idx == torch._C._cuda_getDevice() else torch.cuda.device(idx)
     if stream.device.index != idx:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{idx}")
     return torch.cuda.stream(stream)
 
 
-def _device_of(t, name):
-    idx = t.get_device() if t.is_cuda else -1
-    if idx < 0:
-        raise ValueError(f"libnvq calls take CUDA tensors ({name})")
-    return idx
+def _addresses(idx, *specs):
+    """The addresses of contiguous tensors on device idx; a spec is (name, tensor, dtype, what), what being
+    its shape (a tuple) or the least number of its elements."""
+    out = []
+    for name, t, dtype, what in specs:
+        if (t.dtype is not dtype or t.get_device() != idx or not t.is_contiguous()
+                or (t.shape != what if what.__class__ is tuple else t.numel() < what)):
+            size = f"shape {what}" if isinstance(what, tuple) else f"at least {what} elements"
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{idx} of {size}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+        out.append(t.data_ptr())
+    return out
 
 
-def _handle(idx):
-    """The current stream of device idx as a cudaStream_t."""
-    return torch._C._cuda_getCurrentRawStream(idx)
-
-
-def _need(t, name, idx, dtype, nbytes=0):
-    """The address of a contiguous tensor of this type and at least this size on the call's device."""
-    if t.dtype is not dtype or not t.is_cuda or t.get_device() != idx or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{idx}")
-    if t.nbytes < nbytes:
-        raise ValueError(f"{name} must hold at least {nbytes} bytes")
-    return t.data_ptr()
-
-
-def _need_shape(t, name, idx, dtype, shape):
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    return _need(t, name, idx, dtype)
-
-
-def _need_rows(t, name, idx, M, N):
+def _rows(idx, name, t, M, N):
     """Address and row stride (0: N) of a BF16 [M, N] tensor with contiguous rows."""
-    if t.dtype is not torch.bfloat16 or not t.is_cuda or t.get_device() != idx or t.shape != (M, N):
-        raise ValueError(f"{name} must be a [{M}, {N}] bfloat16 tensor on cuda:{idx}")
+    if t.dtype is not _BF16 or t.get_device() != idx or t.shape != (M, N):
+        raise ValueError(f"{name} must be a [{M}, {N}] bfloat16 tensor on cuda:{idx}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
     if t.is_contiguous():
         return t.data_ptr(), 0
     ld, step = t.stride()
@@ -442,10 +435,20 @@ def _epilogue(idx, M, N, bias, activation, residual, y):
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
-    b = None if bias is None else _need_shape(bias, "bias", idx, torch.bfloat16, (N,))
-    r, ldr = (None, 0) if residual is None else _need_rows(residual, "residual", idx, M, N)
-    yp, ldy = _need_rows(y, "y", idx, M, N)
+    b = None if bias is None else _addresses(idx, ("bias", bias, _BF16, (N,)))[0]
+    r, ldr = (None, 0) if residual is None else _rows(idx, "residual", residual, M, N)
+    yp, ldy = _rows(idx, "y", y, M, N)
     return yp, Epilogue(b, r, ldr, ldy, act)
+
+
+def _matrix(x):
+    if x.dim() != 2:
+        raise ValueError("x must have two dimensions")
+    return x.shape
+
+
+def _padded_scales(rows, K):
+    return (rows + 127) // 128 * 128 * (K // 16)
 
 
 def nvfp4_gemm_w4a4_epilogue(xq, wq, M: int, N: int, K: int, *, bias=None, activation: str = "none", residual=None,
@@ -456,21 +459,22 @@ def nvfp4_gemm_w4a4_epilogue(xq, wq, M: int, N: int, K: int, *, bias=None, activ
     a name of ACTIVATIONS; residual: [M, N] bf16.  residual and y may be views
     with contiguous rows (a row stride that is a multiple of 8), and residual
     may be y: the residual stream updated in place."""
-    idx = _device_of(xq[0], "xq")
+    xc, xs, xt = xq
+    wc, ws, wt = wq
+    idx = xc.get_device()
     away = _elsewhere(idx, stream)
     if away is not None:
         with away:
             return nvfp4_gemm_w4a4_epilogue(xq, wq, M, N, K, bias=bias, activation=activation, residual=residual, y=y)
-    ptrs = []
-    for name, (c, s, t), rows in (("xq", xq, M), ("wq", wq, N)):
-        ptrs += (_need(c, name + " codes", idx, torch.uint8, rows * (K // 2)),
-                 _need(s, name + " scales", idx, torch.uint8, (rows + 127) // 128 * 128 * (K // 16)),
-                 _need(t, name + " t", idx, torch.float32, 4))
+    ptrs = _addresses(idx, ("xq codes", xc, _U8, M * (K // 2)), ("xq scales", xs, _U8, _padded_scales(M, K)),
+                      ("xq t", xt, _F32, 1), ("wq codes", wc, _U8, N * (K // 2)),
+                      ("wq scales", ws, _U8, _padded_scales(N, K)), ("wq t", wt, _F32, 1))
     if y is None:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=xq[0].device)
+        y = torch.empty(M, N, dtype=_BF16, device=xc.device)
     yp, e = _epilogue(idx, M, N, bias, activation, residual, y)
-    _check(lib().nvfp4_gemm_w4a4_epilogue(*ptrs, yp, M, N, K, ctypes.byref(e), _handle(idx)),
-           "nvfp4_gemm_w4a4_epilogue")
+    st = lib().nvfp4_gemm_w4a4_epilogue(*ptrs, yp, M, N, K, ctypes.byref(e), torch._C._cuda_getCurrentRawStream(idx))
+    if st:
+        _check(st, "nvfp4_gemm_w4a4_epilogue")
     return y
 
 
@@ -479,29 +483,28 @@ def w4a16_gemm_epilogue(x, packed_codes, packed_scales, N: int, *, bias=None, ac
     """Y [M, N] bf16 = act(X W^T + bias) + residual for packed INT4 W [N, K]
     (int4_pack_weights).  bias, activation, residual, y as in
     nvfp4_gemm_w4a4_epilogue; x may not overlap y."""
-    idx = _device_of(x, "x")
+    idx = x.get_device()
     away = _elsewhere(idx, stream)
     if away is not None:
         with away:
             return w4a16_gemm_epilogue(x, packed_codes, packed_scales, N, bias=bias, activation=activation,
                                        residual=residual, y=y)
-    if x.dim() != 2:
-        raise ValueError("x must be [M, K]")
-    M, K = x.shape
-    xp = _need(x, "x", idx, torch.bfloat16)
-    pc = _need(packed_codes, "packed_codes", idx, torch.uint8, N * K // 2)
-    ps = _need(packed_scales, "packed_scales", idx, torch.uint8, N * (K // 128) * 2)
+    M, K = _matrix(x)
+    xp, pc, ps = _addresses(idx, ("x", x, _BF16, 0), ("packed_codes", packed_codes, _U8, N * K // 2),
+                            ("packed_scales", packed_scales, _U8, N * (K // 128) * 2))
     if y is None:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+        y = torch.empty(M, N, dtype=_BF16, device=x.device)
     yp, e = _epilogue(idx, M, N, bias, activation, residual, y)
-    _check(lib().w4a16_gemm_epilogue(xp, pc, ps, yp, M, N, K, ctypes.byref(e), _handle(idx)), "w4a16_gemm_epilogue")
+    st = lib().w4a16_gemm_epilogue(xp, pc, ps, yp, M, N, K, ctypes.byref(e), torch._C._cuda_getCurrentRawStream(idx))
+    if st:
+        _check(st, "w4a16_gemm_epilogue")
     return y
 
 
 def nvq_linear_epilogue(x, w4a4=None, w4a16=None, N: int | None = None, *, bias=None, activation: str = "none",
                         residual=None, crossover_m: int = -1, y=None, workspace=None, stream=None):
     """nvq_linear with bias, activation and residual in the product it picks."""
-    idx = _device_of(x, "x")
+    idx = x.get_device()
     away = _elsewhere(idx, stream)
     if away is not None:
         with away:
@@ -509,29 +512,25 @@ def nvq_linear_epilogue(x, w4a4=None, w4a16=None, N: int | None = None, *, bias=
                                        crossover_m=crossover_m, y=y, workspace=workspace)
     if N is None:
         raise ValueError("N is required")
-    if x.dim() != 2:
-        raise ValueError("x must be [M, K]")
-    M, K = x.shape
-    xp = _need(x, "x", idx, torch.bfloat16)
+    M, K = _matrix(x)
+    xp, = _addresses(idx, ("x", x, _BF16, 0))
     w = [None] * 5
     if w4a4 is not None:
         c, s, t = w4a4
-        w[:3] = (_need(c, "w4a4 codes", idx, torch.uint8, N * (K // 2)),
-                 _need(s, "w4a4 scales", idx, torch.uint8, (N + 127) // 128 * 128 * (K // 16)),
-                 _need(t, "w4a4 t", idx, torch.float32, 4))
+        w[:3] = _addresses(idx, ("w4a4 codes", c, _U8, N * (K // 2)), ("w4a4 scales", s, _U8, _padded_scales(N, K)),
+                           ("w4a4 t", t, _F32, 1))
     if w4a16 is not None:
         c, s = w4a16
-        w[3:] = (_need(c, "w4a16 codes", idx, torch.uint8, N * K // 2),
-                 _need(s, "w4a16 scales", idx, torch.uint8, N * (K // 128) * 2))
+        w[3:] = _addresses(idx, ("w4a16 codes", c, _U8, N * K // 2), ("w4a16 scales", s, _U8, N * (K // 128) * 2))
     if y is None:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+        y = torch.empty(M, N, dtype=_BF16, device=x.device)
     need = nvq_linear_workspace_bytes(M, N, K, crossover_m)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    wp, wn = (None, 0) if workspace is None else (_need(workspace, "workspace", idx, workspace.dtype), workspace.nbytes)
+        workspace = torch.empty(need, dtype=_U8, device=x.device)
+    wp, wn = (None, 0) if workspace is None else (*_addresses(idx, ("workspace", workspace, _U8, 0)), workspace.numel())
     yp, e = _epilogue(idx, M, N, bias, activation, residual, y)
-    _check(lib().nvq_linear_epilogue(xp, M, N, K, *w, crossover_m, yp, ctypes.byref(e), wp, wn, _handle(idx)),
-           "nvq_linear_epilogue")
+    _check(lib().nvq_linear_epilogue(xp, M, N, K, *w, crossover_m, yp, ctypes.byref(e), wp, wn,
+                                     torch._C._cuda_getCurrentRawStream(idx)), "nvq_linear_epilogue")
     return y
 
 
@@ -541,40 +540,22 @@ def w4a16_moe_workspace_bytes(T: int, H: int, I: int, topk: int) -> int:
     return int(lib().w4a16_moe_workspace_bytes(T, H, I, topk))
 
 
-def _tokens(x, idx):
-    """(address, T, H) of the layer's input."""
-    if x.dim() != 2:
-        raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    return _need(x, "x", idx, torch.bfloat16), T, H
-
-
-def _choices(x, idx, T, topk, ids, weights):
+def _chosen(x, T, topk, ids, weights):
+    """ids and weights, made where the caller left them out."""
     if ids is None:
-        ids = torch.empty(T, topk, dtype=torch.int32, device=x.device)
+        ids = torch.empty(T, topk, dtype=_I32, device=x.device)
     if weights is None:
-        weights = torch.empty(T, topk, dtype=torch.float32, device=x.device)
-    shape = (T, topk)
-    return (ids, weights, _need_shape(ids, "ids", idx, torch.int32, shape),
-            _need_shape(weights, "weights", idx, torch.float32, shape))
+        weights = torch.empty(T, topk, dtype=_F32, device=x.device)
+    return ids, weights
 
 
-def _experts(x, idx, T, E, H, I, topk, gate_up, down, residual, y, workspace):
-    """Checks the experts' arguments and allocates what the caller left out: (y, workspace, addresses of
-    the four packed tensors, residual and y, address and size of the workspace)."""
-    gc, gs = gate_up
-    dc, ds = down
-    n = E * I * H
-    ptrs = (_need(gc, "gate_up codes", idx, torch.uint8, n), _need(gs, "gate_up scales", idx, torch.uint8, n // 32),
-            _need(dc, "down codes", idx, torch.uint8, n // 2), _need(ds, "down scales", idx, torch.uint8, n // 64))
-    shape = (T, H)
-    r = None if residual is None else _need_shape(residual, "residual", idx, torch.bfloat16, shape)
+def _output(x, T, H, I, topk, y, workspace):
+    """y and workspace, made where the caller left them out."""
     if y is None:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
-    yp = _need_shape(y, "y", idx, torch.bfloat16, shape)
+        y = torch.empty(T, H, dtype=_BF16, device=x.device)
     if workspace is None:
-        workspace = torch.empty(w4a16_moe_workspace_bytes(T, H, I, topk), dtype=torch.uint8, device=x.device)
-    return y, workspace, (*ptrs, r, yp), (_need(workspace, "workspace", idx, workspace.dtype), workspace.nbytes)
+        workspace = torch.empty(w4a16_moe_workspace_bytes(T, H, I, topk), dtype=_U8, device=x.device)
+    return y, workspace
 
 
 def moe_route(x, w_router, topk: int, *, renormalize: bool = True, ids=None, weights=None, stream=None):
@@ -582,16 +563,20 @@ def moe_route(x, w_router, topk: int, *, renormalize: bool = True, ids=None, wei
 
     x [T, H] bf16, w_router [E, H] bf16; softmax over the chosen experts, or
     over all E with renormalize=False."""
-    idx = _device_of(x, "x")
+    idx = x.get_device()
     away = _elsewhere(idx, stream)
     if away is not None:
         with away:
             return moe_route(x, w_router, topk, renormalize=renormalize, ids=ids, weights=weights)
-    xp, T, H = _tokens(x, idx)
+    T, H = _matrix(x)
     E = w_router.shape[0]
-    rp = _need_shape(w_router, "w_router", idx, torch.bfloat16, (E, H))
-    ids, weights, ip, wp = _choices(x, idx, T, topk, ids, weights)
-    _check(lib().moe_route(xp, rp, T, E, H, topk, 1 if renormalize else 0, ip, wp, _handle(idx)), "moe_route")
+    ids, weights = _chosen(x, T, topk, ids, weights)
+    xp, rp, ip, wp = _addresses(idx, ("x", x, _BF16, 0), ("w_router", w_router, _BF16, (E, H)),
+                                ("ids", ids, _I32, (T, topk)), ("weights", weights, _F32, (T, topk)))
+    st = lib().moe_route(xp, rp, T, E, H, topk, 1 if renormalize else 0, ip, wp,
+                         torch._C._cuda_getCurrentRawStream(idx))
+    if st:
+        _check(st, "moe_route")
     return ids, weights
 
 
@@ -603,37 +588,57 @@ def w4a16_moe_experts(x, ids, weights, gate_up, down, E: int, I: int, *, residua
     gate_up, down: (packed_codes, packed_scales) of int4_pack_weights over the
     stacked experts, [E * 2I, H] (each expert interleave_gate_up(..., block=16))
     and [E * H, I].  y may be x or residual."""
-    idx = _device_of(x, "x")
+    idx = x.get_device()
     away = _elsewhere(idx, stream)
     if away is not None:
         with away:
             return w4a16_moe_experts(x, ids, weights, gate_up, down, E, I, residual=residual, y=y, workspace=workspace)
-    xp, T, H = _tokens(x, idx)
+    T, H = _matrix(x)
     if ids.dim() != 2:
         raise ValueError("ids must be [T, topk]")
-    topk = ids.shape[1]
-    _, _, ip, wp = _choices(x, idx, T, topk, ids, weights)
-    y, workspace, ptrs, ws = _experts(x, idx, T, E, H, I, topk, gate_up, down, residual, y, workspace)
-    _check(lib().w4a16_moe_experts(xp, ip, wp, *ptrs, T, E, H, I, topk, *ws, _handle(idx)), "w4a16_moe_experts")
+    topk, n = ids.shape[1], E * I * H
+    gc, gs = gate_up
+    dc, ds = down
+    y, workspace = _output(x, T, H, I, topk, y, workspace)
+    xp, ip, wp, gcp, gsp, dcp, dsp, yp, wsp = _addresses(
+        idx, ("x", x, _BF16, 0), ("ids", ids, _I32, (T, topk)), ("weights", weights, _F32, (T, topk)),
+        ("gate_up codes", gc, _U8, n), ("gate_up scales", gs, _U8, n // 32), ("down codes", dc, _U8, n // 2),
+        ("down scales", ds, _U8, n // 64), ("y", y, _BF16, (T, H)), ("workspace", workspace, _U8, 0))
+    rp = None if residual is None else _addresses(idx, ("residual", residual, _BF16, (T, H)))[0]
+    st = lib().w4a16_moe_experts(xp, ip, wp, gcp, gsp, dcp, dsp, rp, yp, T, E, H, I, topk, wsp, workspace.numel(),
+                                 torch._C._cuda_getCurrentRawStream(idx))
+    if st:
+        _check(st, "w4a16_moe_experts")
     return y
 
 
 def w4a16_moe(x, w_router, gate_up, down, I: int, topk: int, *, renormalize: bool = True, residual=None, ids=None,
               weights=None, y=None, workspace=None, stream=None):
-    """The whole layer: moe_route, then w4a16_moe_experts.  Returns (y, ids, weights)."""
-    idx = _device_of(x, "x")
+    """The whole layer: what moe_route and then w4a16_moe_experts compute, in one
+    launch per 32 tokens.  Returns (y, ids, weights)."""
+    idx = x.get_device()
     away = _elsewhere(idx, stream)
     if away is not None:
         with away:
             return w4a16_moe(x, w_router, gate_up, down, I, topk, renormalize=renormalize, residual=residual, ids=ids,
                              weights=weights, y=y, workspace=workspace)
-    xp, T, H = _tokens(x, idx)
+    T, H = _matrix(x)
     E = w_router.shape[0]
-    rp = _need_shape(w_router, "w_router", idx, torch.bfloat16, (E, H))
-    ids, weights, ip, wp = _choices(x, idx, T, topk, ids, weights)
-    y, workspace, ptrs, ws = _experts(x, idx, T, E, H, I, topk, gate_up, down, residual, y, workspace)
-    _check(lib().w4a16_moe(xp, rp, *ptrs, ip, wp, T, E, H, I, topk, 1 if renormalize else 0, *ws, _handle(idx)),
-           "w4a16_moe")
+    n = E * I * H
+    gc, gs = gate_up
+    dc, ds = down
+    ids, weights = _chosen(x, T, topk, ids, weights)
+    y, workspace = _output(x, T, H, I, topk, y, workspace)
+    xp, rtp, gcp, gsp, dcp, dsp, yp, ip, wp, wsp = _addresses(
+        idx, ("x", x, _BF16, 0), ("w_router", w_router, _BF16, (E, H)), ("gate_up codes", gc, _U8, n),
+        ("gate_up scales", gs, _U8, n // 32), ("down codes", dc, _U8, n // 2), ("down scales", ds, _U8, n // 64),
+        ("y", y, _BF16, (T, H)), ("ids", ids, _I32, (T, topk)), ("weights", weights, _F32, (T, topk)),
+        ("workspace", workspace, _U8, 0))
+    rp = None if residual is None else _addresses(idx, ("residual", residual, _BF16, (T, H)))[0]
+    st = lib().w4a16_moe(xp, rtp, gcp, gsp, dcp, dsp, rp, yp, ip, wp, T, E, H, I, topk, 1 if renormalize else 0, wsp,
+                         workspace.numel(), torch._C._cuda_getCurrentRawStream(idx))
+    if st:
+        _check(st, "w4a16_moe")
     return y, ids, weights
 
 

@@ -332,7 +332,7 @@ struct ExpertParams {
   float* partial;                   // [2 gridDim][T][32]
   uint32_t T, E, H, I, topk;
   uint32_t stage;                   // all of h fits in shared memory
-  FastDiv by_topk, by_grid, by_g, by_rtiles;   // topk, gridDim, H / 128, I / 16
+  FastDiv by_topk, by_grid, by_g, by_rtiles, by_gi;   // topk, gridDim, H / 128, I / 16, I / 128
   // the router phase
   const __nv_bfloat16* wr;          // [E, H]
   float* logits;                    // [slices][T][16 etiles] partial sums
@@ -351,6 +351,13 @@ struct Plan {
   uint8_t token[kMaxPairs];         // slot -> token
   uint32_t warp_sum[EWARPS];
   uint32_t segments;
+};
+
+// How the down phase cuts its work for one CTA.
+struct DownCut {
+  uint32_t half, whole, parts;      // half tiles; whole tiles or half tiles only; parts of the work
+  uint32_t q, r;                    // pieces per part, the first r parts one more
+  uint32_t F0, F1, n0, n1;          // this CTA's units of the flat sequence and its tiles (none: n0 > n1)
 };
 
 // Sorts the pairs of pl.id / pl.w by expert into segments of at most COLS tokens
@@ -561,6 +568,36 @@ __device__ __forceinline__ void unit_products(const Weights& w, const uint4 (&b)
         acc[n][tt][i] = __fmaf_rn(sc[2 * tt + (i >> 1)], GIVEN ? d[n][tt][i] : d[n][tt][i] + o[n][i], acc[n][tt][i]);
 }
 
+// The same for one of the unit's two row tiles (tt), the third chain included.
+template <int NB>
+__device__ __forceinline__ void half_products(const Weights& w, uint32_t tt, const uint4 (&b)[NB][4], float (&acc)[NB][2][4]) {
+  const uint32_t neg[4] = {kNeg136, kNeg136, kNeg136, kNeg136};
+  float o[NB][4], d[NB][4];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint4 v = w.q[j >> 1];
+    uint32_t a[4];
+    w4a16::word_to_frag((j & 1) ? (tt ? v.w : v.z) : (tt ? v.y : v.x), a);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const uint4 q = b[n][j >> 1];
+      const uint32_t b0 = (j & 1) ? q.z : q.x, b1 = (j & 1) ? q.w : q.y;
+      if (j == 0) {
+        w4a16::mma_z(d[n], a, b0, b1);
+        w4a16::mma_z(o[n], neg, b0, b1);
+      } else {
+        w4a16::mma_acc(d[n], a, b0, b1);
+        w4a16::mma_acc(o[n], neg, b0, b1);
+      }
+    }
+  }
+  const uint32_t s = tt ? w.s.y : w.s.x;
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][0][i] = __fmaf_rn((i & 2) ? bf16_hi(s) : bf16_lo(s), d[n][i] + o[n][i], acc[n][0][i]);
+}
+
 // h is kept in the order in which the down phase reads it: inside a group of 128
 // columns, column 32 c + 8 i + e at 32 i + 8 c + e, so that the i-th 16-byte load of
 // the four lanes c takes 64 consecutive bytes.  Where the 16 columns of row tile rt
@@ -577,11 +614,6 @@ __device__ __forceinline__ uint32_t ticket(uint32_t* counter) {
   uint32_t old;
   asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
   return old;
-}
-
-// a / b, in 32 bits where both fit (a 64-bit division is a long subroutine).
-__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
-  return ((a | b) >> 32) == 0 ? (uint64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // ------------------------------------------------------------------ the layer
@@ -601,6 +633,32 @@ constexpr int kCutTiles = EWARPS * 2 * 1024;
 constexpr int layer_smem(int64_t T, int64_t P, int64_t I) {
   const int64_t rows = EWARPS * T * 32 * 4 + (stage_h(T, P, I) ? P * I * 4 : 0), gate = kCutTiles + kOffsets * 32;
   return RING_BYTES + (int)(rows > gate ? rows : gate);
+}
+
+// Down: a round (one unit per warp) takes about 1 us, 0.6 us for one row tile of the
+// unit; joining cut tiles through memory takes about 2.5 us.  So: half tiles (16 columns)
+// where that leaves no more of them than CTAs and is not slower, whole tiles, or even
+// parts of the flat sequence of units.
+__device__ __forceinline__ DownCut cut_down(const ExpertParams& p, uint32_t segments, uint32_t ntile, uint32_t Gi) {
+  DownCut d;
+  const uint32_t U = segments * Gi, total = U * ntile, grid = gridDim.x;
+  const uint32_t rounds = (U + EWARPS - 1) / EWARPS, joined = p.by_grid.div(total / EWARPS) + 3;
+  d.half = 2 * ntile <= grid && rounds * 5 <= joined * 8;
+  d.whole = d.half || p.by_grid.div(ntile + grid - 1) * rounds <= joined;
+  const uint32_t pieces = d.whole ? (d.half ? 2 * ntile : ntile) : total;
+  d.parts = min(grid, d.whole ? pieces : (total + EWARPS - 1) / EWARPS);
+  d.q = d.parts == grid ? p.by_grid.div(pieces) : pieces / max(d.parts, 1u);
+  d.r = pieces - d.q * d.parts;
+  const uint32_t b = blockIdx.x, P0 = b * d.q + min(b, d.r), P1 = P0 + d.q + (b < d.r ? 1u : 0u);
+  d.F0 = d.whole ? P0 * U : P0;
+  d.F1 = d.whole ? P1 * U : P1;
+  d.n0 = 1u;
+  d.n1 = 0u;
+  if (b < d.parts) {
+    d.n0 = d.whole ? P0 : P0 / U;
+    d.n1 = d.whole ? P1 - 1 : (P1 - 1) / U;
+  }
+  return d;
 }
 
 // One 64-wide k block of the router: 16 experts x 8 M tokens, K permuted alike in
@@ -641,6 +699,7 @@ template <bool ROUTE>
 __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t esm[];
   __shared__ Plan pl;
+  __shared__ DownCut cd;
   __shared__ uint32_t last[2];
   const auto grid = cooperative_groups::this_grid();
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g8 = lane >> 2, c = lane & 3u;
@@ -721,17 +780,28 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
     // known numbers.
     constexpr uint32_t kUnitCost = 28;
     const uint32_t slots = segments ? pl.seg_s[segments - 1] + pl.seg_n[segments - 1] : 0u;
-    const uint32_t cost = (kUnitCost * segments + slots) * rtiles, quot = p.by_grid.div(cost), rest = cost - quot * gridDim.x;
-    auto first_tile = [&](uint32_t b) {
+    const bool even = P <= 32;                                         // a few pairs: tiles are cut evenly, which is quicker to find
+    const uint32_t cost = even ? segments * rtiles : (kUnitCost * segments + slots) * rtiles, quot = p.by_grid.div(cost), rest = cost - quot * gridDim.x;
+    uint32_t T0 = 0, mine = 0;                                         // this CTA's tiles
+#pragma unroll 1
+    for (uint32_t b = blockIdx.x; b <= blockIdx.x + 1; ++b) {
       const uint32_t at = b * quot + min(b, rest);
+      if (even) {
+        mine = at - T0;
+        T0 = b == blockIdx.x ? at : T0;
+        continue;
+      }
       uint32_t s = 0;                                                  // segments that begin at or before `at`
       for (uint32_t k = 0; k < segments; k += 32)
         s += __popc(__ballot_sync(0xFFFFFFFFu, k + lane < segments && (kUnitCost * (k + lane) + pl.seg_s[k + lane]) * rtiles <= at));
-      if (s == 0 || at == cost) return segments * rtiles;
-      --s;
-      return s * rtiles + (at - (kUnitCost * s + pl.seg_s[s]) * rtiles) / (kUnitCost + pl.seg_n[s]);
-    };
-    const uint32_t T0 = first_tile(blockIdx.x), mine = first_tile(blockIdx.x + 1) - T0;
+      uint32_t t = segments * rtiles;
+      if (s != 0 && at != cost) {
+        --s;
+        t = s * rtiles + (at - (kUnitCost * s + pl.seg_s[s]) * rtiles) / (kUnitCost + pl.seg_n[s]);
+      }
+      if (b == blockIdx.x) T0 = t;
+      else mine = t - T0;
+    }
     const uint32_t L = mine * G;                                       // this CTA's units
     auto cut = [&](uint32_t w) { return (uint32_t)((uint64_t)L * w / EWARPS); };
     const uint32_t f0 = cut(warp), f1 = cut(warp + 1);
@@ -788,8 +858,12 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
 #pragma unroll
       for (int i = 0; i < 4; ++i) b[i] = __ldg(row + at * 16 + i);
     };
-    // While the first weights are on their way: the column offsets of this CTA's
-    // segments, which each of their row tiles needs again.
+    // While the first weights are on their way: how the down phase is cut, and the
+    // column offsets of this CTA's segments, which each of their row tiles needs again.
+    if (warp == EWARPS - 1) {
+      const DownCut d = cut_down(p, segments, ntile, Gi);
+      if (lane == 0) cd = d;
+    }
     const uint32_t seg0 = p.by_rtiles.div(T0), nseg = mine ? p.by_rtiles.div(T0 + mine - 1) - seg0 + 1 : 0u;
     const bool given = nseg * G <= kOffsets;
     float2* offsets = reinterpret_cast<float2*>(esm + RING_BYTES + kCutTiles);   // [segment][group][c]
@@ -871,35 +945,28 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
   // ---- down
   for (uint32_t i = blockIdx.x * ETHREADS + threadIdx.x; i < ntile; i += gridDim.x * ETHREADS) p.tickets[i] = 0u;
   auto arrived = grid.barrier_arrive();                                // this CTA's h is written
-  const uint32_t U = segments * Gi, outs = T * 32;
-  const uint64_t total = (uint64_t)U * ntile;
-  if (total == 0) {                                                    // no token has an expert
+  const uint32_t U = segments * Gi;
+  if (segments == 0) {                                                 // no token has an expert
     grid.barrier_wait(std::move(arrived));
     for (size_t i = (size_t)blockIdx.x * ETHREADS + threadIdx.x; i < (size_t)T * H; i += (size_t)gridDim.x * ETHREADS)
       p.y[i] = p.residual ? p.residual[i] : __float2bfloat16_rn(0.f);
     return;
   }
-  const bool whole_tiles = U <= 6 * EWARPS;
-  const uint32_t parts = (uint32_t)min((uint64_t)gridDim.x, whole_tiles ? (uint64_t)ntile : (total + EWARPS - 1) / EWARPS);
-  // Part b: units [bound(b), bound(b + 1)) of the flat sequence, whole tiles if `whole_tiles`.
-  const uint64_t items = whole_tiles ? (uint64_t)ntile : total, share_q = quotient(items, parts), share_r = items - share_q * parts;
-  auto bound = [&](uint32_t b) { return (b * share_q + min((uint64_t)b, share_r)) * (whole_tiles ? U : 1u); };
-  const bool works = blockIdx.x < parts;
-  const uint64_t F0 = works ? bound(blockIdx.x) : 0, F1 = works ? bound(blockIdx.x + 1) : 0;
-  const uint32_t n0 = works ? (uint32_t)quotient(F0, U) : 1u, n1 = works ? (uint32_t)quotient(F1 - 1, U) : 0u;
+  const bool half = cd.half != 0;
+  const uint32_t F0 = cd.F0, F1 = cd.F1, n0 = cd.n0, n1 = cd.n1, width = half ? 16u : 32u, outs = T * width;
+  const bool works = n0 <= n1;
   // This warp's share [lo, hi) of the units of tile n that belong to this CTA.
   auto share = [&](uint32_t n, uint32_t& lo, uint32_t& hi) {
-    const uint64_t tb = (uint64_t)n * U;
-    const uint32_t from = (uint32_t)(max(F0, tb) - tb), len = (uint32_t)(min(F1, tb + U) - tb) - from;
+    const uint32_t tb = n * U, from = max(F0, tb) - tb, len = min(F1, tb + U) - tb - from;
     lo = from + (uint32_t)((uint64_t)len * warp / EWARPS);
     hi = from + (uint32_t)((uint64_t)len * (warp + 1) / EWARPS);
   };
   uint32_t rn = n0, rseg = 0, rleft = 0, rem = 0, lo = 0, hi = 0;      // the units being requested
   auto request_from = [&](uint32_t a, uint32_t b) {
     rem = b - a;
-    rseg = a / Gi;
+    rseg = p.by_gi.div(a);
     rleft = Gi - (a - rseg * Gi);
-    if (rem > 0) ring.locate(p.d_codes, p.d_scales, ((size_t)pl.seg_e[rseg] * ntile + rn) * Gi + (Gi - rleft));
+    if (rem > 0) ring.locate(p.d_codes, p.d_scales, ((size_t)pl.seg_e[rseg] * ntile + (half ? rn >> 1 : rn)) * Gi + (Gi - rleft));
   };
   auto fill = [&]() {
     while (rem == 0 && rn < n1) {                                      // on to the next tile's share
@@ -912,7 +979,7 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
       --rem;
       if (--rleft == 0 && rem > 0) {
         rleft = Gi;
-        ring.locate(p.d_codes, p.d_scales, ((size_t)pl.seg_e[++rseg] * ntile + rn) * Gi);
+        ring.locate(p.d_codes, p.d_scales, ((size_t)pl.seg_e[++rseg] * ntile + (half ? rn >> 1 : rn)) * Gi);
       }
     }
     cp_commit();
@@ -926,23 +993,29 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
     for (int i = 0; i < RING; ++i) fill();
   }
   constexpr int OUTS = kMaxTokens * 32 / ETHREADS;                     // outputs of a tile per thread
-  float* sums = reinterpret_cast<float*>(esm + RING_BYTES);            // [EWARPS][T][32]
+  float* sums = reinterpret_cast<float*>(esm + RING_BYTES);            // [EWARPS][T][width]
   float* rows = sums + warp * outs;
-  // The residual of this thread's outputs of tile n, where this CTA finishes it alone.
-  auto residual_of = [&](uint32_t n, float (&r)[OUTS]) {
+  const uint32_t wlog = half ? 4 : 5;
+  auto output_at = [&](uint32_t n, uint32_t i) { return (size_t)(i >> wlog) * H + n * width + (i & (width - 1)); };
+  // The residual of this thread's outputs of tile n (requested, not yet waited for).
+  auto residual_of = [&](uint32_t n, uint16_t (&r)[OUTS]) {
+    if (p.residual)
 #pragma unroll
-    for (int k = 0; k < OUTS; ++k) {
-      const uint32_t i = threadIdx.x + k * ETHREADS;
-      r[k] = p.residual && i < outs ? __bfloat162float(p.residual[(size_t)(i / 32) * H + n * 32 + i % 32]) : 0.f;
-    }
+      for (int k = 0; k < OUTS; ++k) {
+        const uint32_t i = threadIdx.x + k * ETHREADS;
+        if (i < outs) r[k] = reinterpret_cast<const uint16_t*>(p.residual)[output_at(n, i)];
+      }
+  };
+  auto store = [&](uint32_t n, uint32_t i, float v, uint16_t r) {
+    p.y[output_at(n, i)] = __float2bfloat16_rn(v + __uint_as_float((uint32_t)r << 16));   // r = 0 without a residual
   };
   auto clear_rows = [&]() {
     for (uint32_t i = lane; i < outs; i += 32) rows[i] = 0.f;
   };
-  float res[OUTS] = {};
+  uint16_t res[OUTS] = {};
   if (works) {
     clear_rows();
-    if (F0 <= (uint64_t)n0 * U && F1 >= (uint64_t)n0 * U + U) residual_of(n0, res);
+    if (F0 <= n0 * U && F1 >= n0 * U + U) residual_of(n0, res);
   }
   grid.barrier_wait(std::move(arrived));
 
@@ -957,13 +1030,13 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
     __syncthreads();
     h = reinterpret_cast<const __nv_bfloat16*>(to);
   }
-  // The parts with a unit of tile n: b0 .. b1.  The first share_r parts hold one item more.
-  auto owner = [&](uint64_t u) {
-    const uint64_t wide = share_r * (share_q + 1);
-    return (uint32_t)(u < wide ? quotient(u, share_q + 1) : share_r + quotient(u - wide, share_q));
+  // The part with unit u of the flat sequence (cut tiles only): the first r parts hold one unit more.
+  auto owner = [&](uint32_t u) {
+    const uint32_t wide = cd.r * (cd.q + 1);
+    return u < wide ? u / (cd.q + 1) : cd.r + (u - wide) / cd.q;
   };
   for (uint32_t n = n0; n <= n1; ++n) {
-    const uint64_t tb = (uint64_t)n * U;
+    const uint32_t tb = n * U;
     const bool whole = F0 <= tb && F1 >= tb + U;
     if (n > n0) {
       clear_rows();
@@ -975,7 +1048,7 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
       // Columns 0 .. 3 of an MMA tile are the high halves of four tokens' h, columns 4 .. 7
       // the low halves.  A segment of up to four tokens needs one MMA tile: its next unit's
       // h is requested a unit ahead.
-      uint32_t seg = lo / Gi, g = lo - seg * Gi, left = hi - lo, m = 0;
+      uint32_t seg = p.by_gi.div(lo), g = lo - seg * Gi, left = hi - lo, m = 0;
       const __nv_bfloat16* row[2] = {nullptr, nullptr};
       uint4 hv[2][4];
       auto load_h = [&](uint4 (&d)[4], int t, uint32_t at) {
@@ -1004,7 +1077,18 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
           cp_wait<RING - 1>();
           w.read(ring.at, lane);
         };
-        if (tokens <= 4) {
+        if (half) {                                                    // few units: nothing to gain from a second copy of h
+          for (uint32_t k = 0; k < run; ++k) {
+            next();
+            if (tokens <= 4) half_products<1>(w, n & 1u, reinterpret_cast<const uint4 (&)[1][4]>(hv[0]), reinterpret_cast<float (&)[1][2][4]>(acc[0]));
+            else half_products<2>(w, n & 1u, hv, acc);
+            if (k + 1 < run) {
+              load_h(hv[0], 0, g + k + 1);
+              if (tokens > 4) load_h(hv[1], 1, g + k + 1);
+            }
+            fill();
+          }
+        } else if (tokens <= 4) {
           auto one = [&](int t) {
             next();
             unit_products<false, 1>(w, reinterpret_cast<const uint4 (&)[1][4]>(hv[t]), none1, reinterpret_cast<float (&)[1][2][4]>(acc[0]));
@@ -1042,7 +1126,8 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
               const float v0 = acc[t][0][i] + __shfl_xor_sync(0xFFFFFFFFu, acc[t][0][i], 2);
               const float v1 = acc[t][1][i] + __shfl_xor_sync(0xFFFFFFFFu, acc[t][1][i], 2);
               const uint32_t col = 4 * t + 2 * (c & 1u) + (i & 1);
-              if (col < tokens) rows[pl.token[s0 + col] * 32 + g8 + ((i & 2) ? 8 : 0) + (c < 2 ? 0 : 16)] += c < 2 ? v0 : v1;
+              if (col < tokens && (c < 2 || !half))
+                rows[(pl.token[s0 + col] << wlog) + g8 + ((i & 2) ? 8 : 0) + (c < 2 ? 0 : 16)] += c < 2 ? v0 : v1;
             }
           }
         __syncwarp();
@@ -1059,7 +1144,7 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
 #pragma unroll
       for (int k = 0; k < OUTS; ++k) {
         const uint32_t i = threadIdx.x + k * ETHREADS;
-        if (i < outs) p.y[(size_t)(i / 32) * H + n * 32 + i % 32] = __float2bfloat16_rn(warps_sum(i) + res[k]);
+        if (i < outs) store(n, i, warps_sum(i), res[k]);
       }
       __syncthreads();                                                 // the rows are cleared for the next tile
     } else {
@@ -1073,11 +1158,11 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
   __syncthreads();
   // The cut tiles (the first and the last of the range at most) for which this CTA came last.
   for (uint32_t k = 0; k < 2; ++k) {
-    const uint32_t n = k ? n1 : n0;
-    const uint64_t tb = (uint64_t)n * U;
+    const uint32_t n = k ? n1 : n0, tb = n * U;
     if (!works || (k == 1 && n1 == n0) || (F0 <= tb && F1 >= tb + U) || !last[k]) continue;
     const uint32_t b0 = owner(tb), count = owner(tb + U - 1) - b0 + 1;
-    const float* from = p.partial + ((size_t)2 * b0 + (bound(b0) >= tb ? 0 : 1)) * outs;   // later parts begin with this tile
+    const bool inside = b0 * cd.q + min(b0, cd.r) >= tb;               // b0 begins with this tile, as the later parts do
+    const float* from = p.partial + ((size_t)2 * b0 + (inside ? 0 : 1)) * outs;
     residual_of(n, res);
 #pragma unroll
     for (int j = 0; j < OUTS; ++j) {
@@ -1086,7 +1171,7 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
         float s = __ldcg(from + i);
 #pragma unroll 4
         for (uint32_t b = 1; b < count; ++b) s += __ldcg(p.partial + (size_t)2 * (b0 + b) * outs + i);
-        p.y[(size_t)(i / 32) * H + n * 32 + i % 32] = __float2bfloat16_rn(s + res[j]);
+        store(n, i, s, res[j]);
       }
     }
   }

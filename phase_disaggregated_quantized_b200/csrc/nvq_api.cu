@@ -740,7 +740,8 @@ namespace {
 // CTAs of the expert kernel: one on each of a B200's SMs.  A constant, so that the
 // workspace (two partial tiles per CTA) can be sized without a device.
 constexpr int kMoeMaxGrid = 148;
-constexpr int64_t kMoeMaxDim = (int64_t)1 << 20;   // H and I: a CTA's unit counts stay in 32 bits
+// H and I, and one expert's down matrix: units of 512 segments are counted in 31 bits.
+constexpr int64_t kMoeMaxDim = (int64_t)1 << 20, kMoeMaxWeight = (int64_t)1 << 33;
 
 struct MoeWs {
   size_t h, tickets, partial, logits, total;
@@ -823,8 +824,8 @@ nvq_status experts_validate(const char* name, const void* x, const int32_t* ids,
   };
   if (T < 0 || E <= 0 || H <= 0 || I <= 0 || topk <= 0) return bad(NVQ_ERR_INVALID_ARG, "bad sizes");
   if (E > nvq::moe::kMaxExperts || topk > nvq::moe::kMaxTopk) return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "need E <= 512, topk <= 16");
-  if (H % 128 != 0 || I % 128 != 0 || H >= kMoeMaxDim || I >= kMoeMaxDim)
-    return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "need H % 128 == 0, I % 128 == 0, both < 2^20");
+  if (H % 128 != 0 || I % 128 != 0 || H >= kMoeMaxDim || I >= kMoeMaxDim || H * I >= kMoeMaxWeight)
+    return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "need H % 128 == 0, I % 128 == 0, both < 2^20, H * I < 2^33");
   if (T >= kMaxDim) return bad(NVQ_ERR_UNSUPPORTED_SHAPE, "too many tokens");
   if (T == 0) return NVQ_OK;
   if (!x || !ids || !weights || !y) return bad(NVQ_ERR_INVALID_ARG, "NULL pointer");
@@ -874,6 +875,7 @@ nvq_status launch_experts(nvq::moe::ExpertParams p, int64_t T, void* workspace, 
   p.by_grid = FastDiv((uint32_t)grid);
   p.by_g = FastDiv(p.H / 128);
   p.by_rtiles = FastDiv(p.I / 16);
+  p.by_gi = FastDiv(p.I / 128);
   p.etiles = (p.E + 15) / 16;
   // Slices of K of the router: no more (tile, slice) pairs than CTAs, a 64-wide block of K for each warp.
   p.slices = std::max(1u, std::min((uint32_t)grid / p.etiles, p.H / 64 / EWARPS));

@@ -93,7 +93,8 @@ def test_experts_refuse(L):
     assert _experts(L, T=0) == 0
     for kw in (dict(T=-1), dict(E=0), dict(H=0), dict(I=-128), dict(topk=0)):
         assert _experts(L, **kw) == 1, kw
-    for kw in (dict(E=513), dict(topk=17), dict(H=192), dict(I=64), dict(H=1 << 20), dict(I=1 << 20), dict(T=1 << 31)):
+    for kw in (dict(E=513), dict(topk=17), dict(H=192), dict(I=64), dict(H=1 << 20), dict(I=1 << 20), dict(T=1 << 31),
+               dict(H=1 << 17, I=1 << 16)):
         assert _experts(L, **kw) == 2, kw
     for i in (0, 1, 2, 3, 4, 5, 6, 8):
         assert _experts(L, null=i) == 1, i
@@ -205,8 +206,11 @@ def cut(n, w, parts):
     return n * w // parts
 
 
-def first_tile(segs, rtiles, grid, b):
+def first_tile(segs, rtiles, grid, b, pairs):
     slots = segs[-1][1] + segs[-1][2] if segs else 0
+    if pairs <= 32:
+        tiles = len(segs) * rtiles
+        return b * (tiles // grid) + min(b, tiles % grid)
     cost = (UNIT_COST * len(segs) + slots) * rtiles
     quot, rest = cost // grid, cost % grid
     at = b * quot + min(b, rest)
@@ -223,7 +227,7 @@ def test_gate_up_split_covers_every_unit_once():
         ids, E = _random_ids(nrng)
         segs, _ = plan(ids, E)
         rtiles, G, grid = rng.choice([8, 16, 40, 88]), rng.choice([1, 2, 9, 16, 40]), rng.choice([1, 7, GRID])
-        bounds = [first_tile(segs, rtiles, grid, b) for b in range(grid + 1)]
+        bounds = [first_tile(segs, rtiles, grid, b, ids.size) for b in range(grid + 1)]
         assert bounds == sorted(bounds) and bounds[-1] == len(segs) * rtiles and (not segs or bounds[0] == 0)
         for b in rng.sample(range(grid), min(grid, 6)):
             mine = bounds[b + 1] - bounds[b]
@@ -265,21 +269,39 @@ def test_gate_up_split_covers_every_unit_once():
             assert not slots and finished | direct == set(range(mine)) and not finished & direct
 
 
+def down_cut(U, ntile, grid, b):
+    """(half, whole, parts, q, r, F0, F1, n0, n1) of CTA b."""
+    total, rounds = U * ntile, -(-U // WARPS)
+    joined = total // WARPS // grid + 3
+    half = 2 * ntile <= grid and rounds * 5 <= joined * 8
+    whole = half or -(-ntile // grid) * rounds <= joined
+    pieces = (2 * ntile if half else ntile) if whole else total
+    parts = min(grid, pieces if whole else -(-total // WARPS))
+    q, r = pieces // parts, pieces % parts
+    P0, P1 = b * q + min(b, r), (b + 1) * q + min(b + 1, r)
+    k = U if whole else 1
+    n0, n1 = (P0 // (U if not whole else 1), (P1 - 1) // (U if not whole else 1)) if b < parts else (1, 0)
+    return half, whole, parts, q, r, P0 * k, P1 * k, n0, n1
+
+
 def test_down_split_covers_every_unit_once_and_finds_every_part():
     rng = random.Random(3)
-    for _ in range(500):
-        grid, tiles, U = rng.choice([2, GRID]), rng.choice([4, 8, 64, 128, 160]), rng.choice([1, 2, 3, 12, 48, 96, 97, 672])
-        total, whole_tiles = tiles * U, U <= 6 * WARPS
-        parts = min(grid, tiles if whole_tiles else -(-total // WARPS))
-        items = tiles if whole_tiles else total
-        q, r = divmod(items, parts)
-        bound = lambda b: (b * q + min(b, r)) * (U if whole_tiles else 1)                # noqa: E731
+    modes = set()
+    for _ in range(600):
+        grid, ntile, U = rng.choice([2, GRID]), rng.choice([4, 8, 64, 74, 75, 128, 160]), rng.choice([1, 2, 3, 12, 48, 96, 97, 672])
+        half, whole_mode, parts, q, r, *_ = down_cut(U, ntile, grid, 0)
+        modes.add((half, whole_mode))
+        tiles = 2 * ntile if half else ntile
         owner = lambda u: u // (q + 1) if u < r * (q + 1) else r + (u - r * (q + 1)) // q   # noqa: E731
-        count, slot_of, whole = {}, {}, set()
-        for b in range(parts):
-            F0, F1 = bound(b), bound(b + 1)
-            assert F1 > F0 and (b > 0 or F0 == 0)
-            n0, n1, cut_tiles = F0 // U, (F1 - 1) // U, []
+        bound = lambda b: (b * q + min(b, r))                                            # noqa: E731
+        count, slot_of, whole, end = {}, {}, set(), 0
+        for b in range(grid):
+            *_, F0, F1, n0, n1 = down_cut(U, ntile, grid, b)
+            if n0 > n1:
+                assert b >= parts
+                continue
+            assert F0 == end and F1 > F0 and n0 == F0 // U and n1 == (F1 - 1) // U
+            end, cut_tiles = F1, []
             for n in range(n0, n1 + 1):
                 tb = n * U
                 if F0 <= tb and F1 >= tb + U:
@@ -298,8 +320,8 @@ def test_down_split_covers_every_unit_once_and_finds_every_part():
                     assert lo + size * w // WARPS == at
                     at = lo + size * (w + 1) // WARPS
                 assert at == lo + size
-            assert set(cut_tiles) <= {n0, n1} and not (whole_tiles and cut_tiles)
-        assert bound(parts) == total
+            assert set(cut_tiles) <= {n0, n1} and not (whole_mode and cut_tiles)
+        assert end == tiles * U
         assert whole | set(count) == set(range(tiles)) and not whole & set(count)
         for n, c in count.items():
             tb = n * U
@@ -308,6 +330,7 @@ def test_down_split_covers_every_unit_once_and_finds_every_part():
             for b in range(b0, b1 + 1):
                 s = 2 * b + ((0 if bound(b0) >= tb else 1) if b == b0 else 0)
                 assert slot_of[s] == n
+    assert modes == {(True, True), (False, True), (False, False)}
 
 
 def h_at(column):
