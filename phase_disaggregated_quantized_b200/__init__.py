@@ -17,7 +17,7 @@ ending in ``_epilogue`` add bias, activation and residual to those products.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 import re
 
@@ -25,6 +25,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libnvq.so")
+BINDING_PATH = os.path.join(_PKG, "_binding.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "nvq.h")
 
 _lib = None
@@ -386,69 +387,49 @@ def nvq_linear(x, w4a4=None, w4a16=None, N: int | None = None, *, crossover_m: i
 
 
 # ------------------------------------------------------------------ products with an epilogue
-# These calls take a few microseconds on the GPU, so the binding looks at each
-# tensor once and takes the stream's handle without making a stream object.
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+# These calls take a few microseconds on the GPU, so their tensors are checked
+# and their arguments passed on by a compiled binding (csrc/binding.cpp), which
+# calls the same C entry points of libnvq.so.
+_fast = None
 
 
-def _elsewhere(idx, stream):
-    """None if a call on tensors of device idx can be made as things are: the device is current and
-    no stream is named.  Else the context to make it in (what it allocates then belongs to that stream)."""
-    if idx < 0:
-        raise ValueError("libnvq calls take CUDA tensors")
+def _load_binding():
+    """The compiled binding, bound to the loaded library (raises if it has not been built)."""
+    global _fast
+    if _fast is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"_binding.so not built at {BINDING_PATH}; run "
+                               "`python -m phase_disaggregated_quantized_b200.build_lib`")
+        L = lib()
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.bind(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+            "nvfp4_gemm_w4a4_epilogue", "w4a16_gemm_epilogue", "nvq_linear_epilogue", "nvq_linear_workspace_bytes",
+            "moe_route", "w4a16_moe_workspace_bytes", "w4a16_moe_experts", "w4a16_moe")))
+        _fast = m
+    return _fast
+
+
+def _call(fn, stream, first, *args):
+    """One call of the binding, on `stream` (whose device must be that of the tensor `first`) or the current one."""
     if stream is None:
-        return None if idx == torch._C._cuda_getDevice() else torch.cuda.device(idx)
-    if stream.device.index != idx:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{idx}")
-    return torch.cuda.stream(stream)
+        r = getattr(_fast or _load_binding(), fn)(*args)
+    else:
+        if stream.device != first.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+        with torch.cuda.stream(stream):              # what the call allocates belongs to that stream
+            r = getattr(_fast or _load_binding(), fn)(*args)
+    if r.__class__ is int:
+        _check(r, fn)
+    return r
 
 
-def _addresses(idx, *specs):
-    """The addresses of contiguous tensors on device idx; a spec is (name, tensor, dtype, what), what being
-    its shape (a tuple) or the least number of its elements."""
-    out = []
-    for name, t, dtype, what in specs:
-        if (t.dtype is not dtype or t.get_device() != idx or not t.is_contiguous()
-                or (t.shape != what if what.__class__ is tuple else t.numel() < what)):
-            size = f"shape {what}" if isinstance(what, tuple) else f"at least {what} elements"
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{idx} of {size}, "
-                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
-        out.append(t.data_ptr())
-    return out
-
-
-def _rows(idx, name, t, M, N):
-    """Address and row stride (0: N) of a BF16 [M, N] tensor with contiguous rows."""
-    if t.dtype is not _BF16 or t.get_device() != idx or t.shape != (M, N):
-        raise ValueError(f"{name} must be a [{M}, {N}] bfloat16 tensor on cuda:{idx}, "
-                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
-    if t.is_contiguous():
-        return t.data_ptr(), 0
-    ld, step = t.stride()
-    if step != 1 and N > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), ld if M > 1 else 0
-
-
-def _epilogue(idx, M, N, bias, activation, residual, y):
-    """(address of y, nvq_epilogue)."""
-    act = ACTIVATIONS.get(activation)
+def _activation(name):
+    act = ACTIVATIONS.get(name)
     if act is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
-    b = None if bias is None else _addresses(idx, ("bias", bias, _BF16, (N,)))[0]
-    r, ldr = (None, 0) if residual is None else _rows(idx, "residual", residual, M, N)
-    yp, ldy = _rows(idx, "y", y, M, N)
-    return yp, Epilogue(b, r, ldr, ldy, act)
-
-
-def _matrix(x):
-    if x.dim() != 2:
-        raise ValueError("x must have two dimensions")
-    return x.shape
-
-
-def _padded_scales(rows, K):
-    return (rows + 127) // 128 * 128 * (K // 16)
+    return act
 
 
 def nvfp4_gemm_w4a4_epilogue(xq, wq, M: int, N: int, K: int, *, bias=None, activation: str = "none", residual=None,
@@ -459,23 +440,8 @@ def nvfp4_gemm_w4a4_epilogue(xq, wq, M: int, N: int, K: int, *, bias=None, activ
     a name of ACTIVATIONS; residual: [M, N] bf16.  residual and y may be views
     with contiguous rows (a row stride that is a multiple of 8), and residual
     may be y: the residual stream updated in place."""
-    xc, xs, xt = xq
-    wc, ws, wt = wq
-    idx = xc.get_device()
-    away = _elsewhere(idx, stream)
-    if away is not None:
-        with away:
-            return nvfp4_gemm_w4a4_epilogue(xq, wq, M, N, K, bias=bias, activation=activation, residual=residual, y=y)
-    ptrs = _addresses(idx, ("xq codes", xc, _U8, M * (K // 2)), ("xq scales", xs, _U8, _padded_scales(M, K)),
-                      ("xq t", xt, _F32, 1), ("wq codes", wc, _U8, N * (K // 2)),
-                      ("wq scales", ws, _U8, _padded_scales(N, K)), ("wq t", wt, _F32, 1))
-    if y is None:
-        y = torch.empty(M, N, dtype=_BF16, device=xc.device)
-    yp, e = _epilogue(idx, M, N, bias, activation, residual, y)
-    st = lib().nvfp4_gemm_w4a4_epilogue(*ptrs, yp, M, N, K, ctypes.byref(e), torch._C._cuda_getCurrentRawStream(idx))
-    if st:
-        _check(st, "nvfp4_gemm_w4a4_epilogue")
-    return y
+    return _call("nvfp4_gemm_w4a4_epilogue", stream, xq[0], xq, wq, M, N, K, bias, _activation(activation),
+                 residual, y)
 
 
 def w4a16_gemm_epilogue(x, packed_codes, packed_scales, N: int, *, bias=None, activation: str = "none",
@@ -483,79 +449,22 @@ def w4a16_gemm_epilogue(x, packed_codes, packed_scales, N: int, *, bias=None, ac
     """Y [M, N] bf16 = act(X W^T + bias) + residual for packed INT4 W [N, K]
     (int4_pack_weights).  bias, activation, residual, y as in
     nvfp4_gemm_w4a4_epilogue; x may not overlap y."""
-    idx = x.get_device()
-    away = _elsewhere(idx, stream)
-    if away is not None:
-        with away:
-            return w4a16_gemm_epilogue(x, packed_codes, packed_scales, N, bias=bias, activation=activation,
-                                       residual=residual, y=y)
-    M, K = _matrix(x)
-    xp, pc, ps = _addresses(idx, ("x", x, _BF16, 0), ("packed_codes", packed_codes, _U8, N * K // 2),
-                            ("packed_scales", packed_scales, _U8, N * (K // 128) * 2))
-    if y is None:
-        y = torch.empty(M, N, dtype=_BF16, device=x.device)
-    yp, e = _epilogue(idx, M, N, bias, activation, residual, y)
-    st = lib().w4a16_gemm_epilogue(xp, pc, ps, yp, M, N, K, ctypes.byref(e), torch._C._cuda_getCurrentRawStream(idx))
-    if st:
-        _check(st, "w4a16_gemm_epilogue")
-    return y
+    return _call("w4a16_gemm_epilogue", stream, x, x, (packed_codes, packed_scales), N, bias,
+                 _activation(activation), residual, y)
 
 
 def nvq_linear_epilogue(x, w4a4=None, w4a16=None, N: int | None = None, *, bias=None, activation: str = "none",
                         residual=None, crossover_m: int = -1, y=None, workspace=None, stream=None):
     """nvq_linear with bias, activation and residual in the product it picks."""
-    idx = x.get_device()
-    away = _elsewhere(idx, stream)
-    if away is not None:
-        with away:
-            return nvq_linear_epilogue(x, w4a4, w4a16, N, bias=bias, activation=activation, residual=residual,
-                                       crossover_m=crossover_m, y=y, workspace=workspace)
     if N is None:
         raise ValueError("N is required")
-    M, K = _matrix(x)
-    xp, = _addresses(idx, ("x", x, _BF16, 0))
-    w = [None] * 5
-    if w4a4 is not None:
-        c, s, t = w4a4
-        w[:3] = _addresses(idx, ("w4a4 codes", c, _U8, N * (K // 2)), ("w4a4 scales", s, _U8, _padded_scales(N, K)),
-                           ("w4a4 t", t, _F32, 1))
-    if w4a16 is not None:
-        c, s = w4a16
-        w[3:] = _addresses(idx, ("w4a16 codes", c, _U8, N * K // 2), ("w4a16 scales", s, _U8, N * (K // 128) * 2))
-    if y is None:
-        y = torch.empty(M, N, dtype=_BF16, device=x.device)
-    need = nvq_linear_workspace_bytes(M, N, K, crossover_m)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=_U8, device=x.device)
-    wp, wn = (None, 0) if workspace is None else (*_addresses(idx, ("workspace", workspace, _U8, 0)), workspace.numel())
-    yp, e = _epilogue(idx, M, N, bias, activation, residual, y)
-    _check(lib().nvq_linear_epilogue(xp, M, N, K, *w, crossover_m, yp, ctypes.byref(e), wp, wn,
-                                     torch._C._cuda_getCurrentRawStream(idx)), "nvq_linear_epilogue")
-    return y
+    return _call("nvq_linear_epilogue", stream, x, x, w4a4, w4a16, N, bias, _activation(activation),
+                 residual, crossover_m, y, workspace)
 
 
 # ------------------------------------------------------------------ mixture of experts
-@functools.lru_cache(maxsize=256)
 def w4a16_moe_workspace_bytes(T: int, H: int, I: int, topk: int) -> int:
     return int(lib().w4a16_moe_workspace_bytes(T, H, I, topk))
-
-
-def _chosen(x, T, topk, ids, weights):
-    """ids and weights, made where the caller left them out."""
-    if ids is None:
-        ids = torch.empty(T, topk, dtype=_I32, device=x.device)
-    if weights is None:
-        weights = torch.empty(T, topk, dtype=_F32, device=x.device)
-    return ids, weights
-
-
-def _output(x, T, H, I, topk, y, workspace):
-    """y and workspace, made where the caller left them out."""
-    if y is None:
-        y = torch.empty(T, H, dtype=_BF16, device=x.device)
-    if workspace is None:
-        workspace = torch.empty(w4a16_moe_workspace_bytes(T, H, I, topk), dtype=_U8, device=x.device)
-    return y, workspace
 
 
 def moe_route(x, w_router, topk: int, *, renormalize: bool = True, ids=None, weights=None, stream=None):
@@ -563,21 +472,7 @@ def moe_route(x, w_router, topk: int, *, renormalize: bool = True, ids=None, wei
 
     x [T, H] bf16, w_router [E, H] bf16; softmax over the chosen experts, or
     over all E with renormalize=False."""
-    idx = x.get_device()
-    away = _elsewhere(idx, stream)
-    if away is not None:
-        with away:
-            return moe_route(x, w_router, topk, renormalize=renormalize, ids=ids, weights=weights)
-    T, H = _matrix(x)
-    E = w_router.shape[0]
-    ids, weights = _chosen(x, T, topk, ids, weights)
-    xp, rp, ip, wp = _addresses(idx, ("x", x, _BF16, 0), ("w_router", w_router, _BF16, (E, H)),
-                                ("ids", ids, _I32, (T, topk)), ("weights", weights, _F32, (T, topk)))
-    st = lib().moe_route(xp, rp, T, E, H, topk, 1 if renormalize else 0, ip, wp,
-                         torch._C._cuda_getCurrentRawStream(idx))
-    if st:
-        _check(st, "moe_route")
-    return ids, weights
+    return _call("moe_route", stream, x, x, w_router, topk, renormalize, ids, weights)
 
 
 def w4a16_moe_experts(x, ids, weights, gate_up, down, E: int, I: int, *, residual=None, y=None, workspace=None,
@@ -588,58 +483,16 @@ def w4a16_moe_experts(x, ids, weights, gate_up, down, E: int, I: int, *, residua
     gate_up, down: (packed_codes, packed_scales) of int4_pack_weights over the
     stacked experts, [E * 2I, H] (each expert interleave_gate_up(..., block=16))
     and [E * H, I].  y may be x or residual."""
-    idx = x.get_device()
-    away = _elsewhere(idx, stream)
-    if away is not None:
-        with away:
-            return w4a16_moe_experts(x, ids, weights, gate_up, down, E, I, residual=residual, y=y, workspace=workspace)
-    T, H = _matrix(x)
-    if ids.dim() != 2:
-        raise ValueError("ids must be [T, topk]")
-    topk, n = ids.shape[1], E * I * H
-    gc, gs = gate_up
-    dc, ds = down
-    y, workspace = _output(x, T, H, I, topk, y, workspace)
-    xp, ip, wp, gcp, gsp, dcp, dsp, yp, wsp = _addresses(
-        idx, ("x", x, _BF16, 0), ("ids", ids, _I32, (T, topk)), ("weights", weights, _F32, (T, topk)),
-        ("gate_up codes", gc, _U8, n), ("gate_up scales", gs, _U8, n // 32), ("down codes", dc, _U8, n // 2),
-        ("down scales", ds, _U8, n // 64), ("y", y, _BF16, (T, H)), ("workspace", workspace, _U8, 0))
-    rp = None if residual is None else _addresses(idx, ("residual", residual, _BF16, (T, H)))[0]
-    st = lib().w4a16_moe_experts(xp, ip, wp, gcp, gsp, dcp, dsp, rp, yp, T, E, H, I, topk, wsp, workspace.numel(),
-                                 torch._C._cuda_getCurrentRawStream(idx))
-    if st:
-        _check(st, "w4a16_moe_experts")
-    return y
+    return _call("w4a16_moe_experts", stream, x, x, ids, weights, gate_up, down, E, I, residual, y,
+                 workspace)
 
 
 def w4a16_moe(x, w_router, gate_up, down, I: int, topk: int, *, renormalize: bool = True, residual=None, ids=None,
               weights=None, y=None, workspace=None, stream=None):
     """The whole layer: what moe_route and then w4a16_moe_experts compute, in one
     launch per 32 tokens.  Returns (y, ids, weights)."""
-    idx = x.get_device()
-    away = _elsewhere(idx, stream)
-    if away is not None:
-        with away:
-            return w4a16_moe(x, w_router, gate_up, down, I, topk, renormalize=renormalize, residual=residual, ids=ids,
-                             weights=weights, y=y, workspace=workspace)
-    T, H = _matrix(x)
-    E = w_router.shape[0]
-    n = E * I * H
-    gc, gs = gate_up
-    dc, ds = down
-    ids, weights = _chosen(x, T, topk, ids, weights)
-    y, workspace = _output(x, T, H, I, topk, y, workspace)
-    xp, rtp, gcp, gsp, dcp, dsp, yp, ip, wp, wsp = _addresses(
-        idx, ("x", x, _BF16, 0), ("w_router", w_router, _BF16, (E, H)), ("gate_up codes", gc, _U8, n),
-        ("gate_up scales", gs, _U8, n // 32), ("down codes", dc, _U8, n // 2), ("down scales", ds, _U8, n // 64),
-        ("y", y, _BF16, (T, H)), ("ids", ids, _I32, (T, topk)), ("weights", weights, _F32, (T, topk)),
-        ("workspace", workspace, _U8, 0))
-    rp = None if residual is None else _addresses(idx, ("residual", residual, _BF16, (T, H)))[0]
-    st = lib().w4a16_moe(xp, rtp, gcp, gsp, dcp, dsp, rp, yp, ip, wp, T, E, H, I, topk, 1 if renormalize else 0, wsp,
-                         workspace.numel(), torch._C._cuda_getCurrentRawStream(idx))
-    if st:
-        _check(st, "w4a16_moe")
-    return y, ids, weights
+    return _call("w4a16_moe", stream, x, x, w_router, gate_up, down, I, topk, renormalize, residual, ids,
+                 weights, y, workspace)
 
 
 def _stream_layers(layers):
