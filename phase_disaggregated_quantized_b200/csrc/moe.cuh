@@ -38,22 +38,23 @@ constexpr int RWARPS = 16;
 constexpr int RTHREADS = RWARPS * 32;
 constexpr int RCHUNK = 8;           // 64-wide k blocks of x staged at a time
 constexpr int RXROW = RCHUNK * 128 + 16;                               // bytes of a staged row (padded: no bank conflicts)
-constexpr int RMINE = kMaxTokens / RCS;                                // tokens that one CTA selects for
 
+// NTK: 8-token MMA tiles of one cluster.
+template <int NTK>
 struct RouteShape {
+  static constexpr int TOKENS = 8 * NTK;
+  static constexpr int MINE = (TOKENS + RCS - 1) / RCS;                // tokens that one CTA selects for
   int etiles, ksub;                 // 16-expert tiles; how many warps share a tile's K range
   __host__ __device__ explicit RouteShape(int E) {
     etiles = (E + 15) / 16;
     ksub = etiles >= RWARPS ? 1 : RWARPS / etiles;
   }
   __host__ __device__ int e16() const { return etiles * 16; }
-  __host__ __device__ int plane() const { return kMaxTokens * e16(); }              // floats
-  __host__ __device__ int smem() const { return 4 * (ksub * plane() + RMINE * e16()) + kMaxTokens * RXROW; }
-  // The planes are largest for the most experts (one plane) or just under
-  // RWARPS expert tiles' worth of rows (at most RWARPS tiles over all planes).
-  static constexpr int max_smem() {
-    return 4 * (kMaxTokens * kMaxExperts + RMINE * kMaxExperts) + kMaxTokens * RXROW;
-  }
+  __host__ __device__ int plane() const { return TOKENS * e16(); }                  // floats
+  __host__ __device__ int smem() const { return 4 * (ksub * plane() + MINE * e16()) + TOKENS * RXROW; }
+  // The planes are largest for the most experts (one plane): fewer than RWARPS
+  // tiles have at most RWARPS tiles over all planes.
+  static constexpr int max_smem() { return 4 * (TOKENS * kMaxExperts + MINE * kMaxExperts) + TOKENS * RXROW; }
 };
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t saddr, uint32_t rank) {
@@ -137,29 +138,34 @@ __device__ __forceinline__ void select_experts(const float* l, uint32_t planes, 
     select_topk<KPL>(sum, E, topk, renorm, lane, id, weight);
   };
   if (E <= 128) with(std::integral_constant<int, 4>());
+  else if (E <= 256) with(std::integral_constant<int, 8>());
   else with(std::integral_constant<int, kMaxExperts / 32>());
 }
 
-// One cluster per 32 tokens.  CTA r multiplies the r-th part of K for all
+// One cluster per 8 NTK tokens.  CTA r multiplies the r-th part of K for all
 // experts and tokens with m16n8k16 MMAs (experts as rows, tokens as columns),
 // each MMA starting from zero and added in FP32, so that no long chain of
 // tensor-core additions truncates.  The partial logits stay in shared memory;
 // after a cluster barrier CTA r adds, in a fixed order, those of the tokens
 // r, r + 16 and one warp per token selects.  The first router weights are
-// requested before the wait on the preceding kernel.
+// requested before the wait on the preceding kernel.  With many tokens the MMAs
+// and their FP32 sums on 16 SMs decide (32 tokens, 384 experts, H 5120: 9 of 16 us), so
+// tokens are spread over clusters of eight as long as the device holds those at once.
+template <int NTK>
 __global__ void __launch_bounds__(RTHREADS, 1)
 route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ wr, uint32_t T, uint32_t E,
              uint32_t H, uint32_t topk, uint32_t renorm, int32_t* __restrict__ ids, float* __restrict__ weights) {
   extern __shared__ __align__(16) float rsm[];
-  const RouteShape sh((int)E);
+  using S = RouteShape<NTK>;
+  const S sh((int)E);
   const uint32_t e16 = sh.e16(), ksub = sh.ksub, plane = sh.plane();
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g = lane >> 2, c = lane & 3u;
   const uint32_t rank = w4a16::cluster_rank();
-  const uint32_t t0 = w4a16::cluster_id() * kMaxTokens, nt = min((uint32_t)kMaxTokens, T - t0);
+  const uint32_t t0 = w4a16::cluster_id() * S::TOKENS, nt = min((uint32_t)S::TOKENS, T - t0);
   const uint32_t nblk = H / 64, b0 = nblk * rank / RCS, b1 = nblk * (rank + 1) / RCS;
   const uint32_t ntile = (nt + 7) / 8;
-  float* logits = rsm + ksub * plane;                                  // [RMINE][e16], this CTA's tokens
-  uint8_t* xs = reinterpret_cast<uint8_t*>(logits + RMINE * e16);
+  float* logits = rsm + ksub * plane;                                  // [MINE][e16], this CTA's tokens
+  uint8_t* xs = reinterpret_cast<uint8_t*>(logits + S::MINE * e16);
   const uint32_t per = min((uint32_t)sh.etiles, (uint32_t)RWARPS);     // warps side by side over the expert tiles
   const uint32_t ks = warp / per, et0 = warp % per;
   const bool active = ks < ksub;
@@ -204,13 +210,13 @@ route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restric
           __ldg(reinterpret_cast<const uint4*>(x + (size_t)(t0 + t) * H + (size_t)c0 * 64) + w);
     }
     __syncthreads();
-    float acc[4][4] = {};
+    float acc[NTK][4] = {};
     uint32_t et = et0, b = k0;
     auto flush = [&]() {                                               // the partial logits of tile et
       float* p = rsm + ks * plane + et * 16 + g;
 #pragma unroll
-      for (int m = 0; m < 4; ++m)
-        if ((uint32_t)m < ntile)
+      for (int m = 0; m < NTK; ++m)
+        if (NTK == 1 || (uint32_t)m < ntile)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float* q = p + (8 * m + 2 * c + (e & 1)) * e16 + (e & 2) * 4;
@@ -229,8 +235,8 @@ route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restric
           // Columns past the last token hold whatever was staged there; nothing reads them.
           const uint8_t* xb = xs + g * RXROW + (b - c0) * 128 + 32 * c;
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
-            if ((uint32_t)m < ntile) {
+          for (int m = 0; m < NTK; ++m)
+            if (NTK == 1 || (uint32_t)m < ntile) {
               const uint4 q0 = *reinterpret_cast<const uint4*>(xb + m * 8 * RXROW);
               const uint4 q1 = *reinterpret_cast<const uint4*>(xb + m * 8 * RXROW + 16);
               float d[4][4];

@@ -843,17 +843,28 @@ nvq_status experts_validate(const char* name, const void* x, const int32_t* ids,
   return NVQ_OK;
 }
 
-nvq_status launch_route(const void* x, const void* wr, int64_t T, int64_t E, int64_t H, int topk, bool renorm,
-                        int32_t* ids, float* weights, cudaStream_t stream) {
+template <int NTK>
+nvq_status launch_route_as(const void* x, const void* wr, int64_t T, int64_t E, int64_t H, int topk, bool renorm,
+                           int32_t* ids, float* weights, cudaStream_t stream) {
   using namespace nvq::moe;
+  using S = RouteShape<NTK>;
   static std::once_flag once[kMaxDevices];
   static cudaError_t err[kMaxDevices];
-  const nvq_status st = kernel_opt_in(route_kernel, RouteShape::max_smem(), RCS > 8, once, err, "moe_route: kernel attributes");
+  const nvq_status st = kernel_opt_in(route_kernel<NTK>, S::max_smem(), RCS > 8, once, err, "moe_route: kernel attributes");
   if (st != NVQ_OK) return st;
-  const int64_t clusters = (T + kMaxTokens - 1) / kMaxTokens;
-  return launch_dependent("route_kernel", route_kernel, (int)(clusters * RCS), RTHREADS, RouteShape((int)E).smem(), RCS,
+  const int64_t clusters = (T + S::TOKENS - 1) / S::TOKENS;
+  return launch_dependent("route_kernel", route_kernel<NTK>, (int)(clusters * RCS), RTHREADS, S((int)E).smem(), RCS,
                           stream, static_cast<const __nv_bfloat16*>(x), static_cast<const __nv_bfloat16*>(wr),
                           (uint32_t)T, (uint32_t)E, (uint32_t)H, (uint32_t)topk, renorm ? 1u : 0u, ids, weights);
+}
+
+// A B200 holds seven clusters of 16 CTAs at once: eight tokens each up to 56, then
+// 16, then 32 (the weights are read once per cluster).
+nvq_status launch_route(const void* x, const void* wr, int64_t T, int64_t E, int64_t H, int topk, bool renorm,
+                        int32_t* ids, float* weights, cudaStream_t stream) {
+  if (T <= 56) return launch_route_as<1>(x, wr, T, E, H, topk, renorm, ids, weights, stream);
+  if (T <= 112) return launch_route_as<2>(x, wr, T, E, H, topk, renorm, ids, weights, stream);
+  return launch_route_as<4>(x, wr, T, E, H, topk, renorm, ids, weights, stream);
 }
 
 // 32 tokens at a time, one cooperative launch each.

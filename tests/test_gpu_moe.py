@@ -49,7 +49,8 @@ def _check_route(x, wr, topk, renorm, ids, weights):
 
 @pytest.mark.parametrize("T, E, H, topk", [
     (1, 1, 64, 1), (1, 128, 4096, 8), (2, 2, 128, 2), (5, 17, 192, 16), (8, 60, 2048, 4), (31, 128, 704, 8),
-    (32, 384, 1024, 6), (33, 512, 256, 16), (64, 16, 512, 1), (70, 8, 8192, 2), (3, 257, 320, 5)])
+    (32, 384, 1024, 6), (33, 512, 256, 16), (56, 200, 640, 3), (64, 16, 512, 1), (70, 8, 8192, 2), (3, 257, 320, 5), (113, 130, 192, 4),
+    (300, 512, 128, 2)])
 def test_route_matches_the_oracle(T, E, H, topk):
     g = torch.Generator().manual_seed(T + E + H)
     x = synth.activations(T, H, seed=T)
