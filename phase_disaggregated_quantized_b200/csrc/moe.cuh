@@ -57,12 +57,6 @@ struct RouteShape {
   static constexpr int max_smem() { return 4 * (TOKENS * kMaxExperts + MINE * kMaxExperts) + TOKENS * RXROW; }
 };
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t saddr, uint32_t rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(w4a16::map_to_rank(saddr, rank)) : "memory");
-  return v;
-}
 // Unsigned order of the result = order of the logits; every NaN is above all
 // numbers, -0 equals +0, and 0 is below every logit (no expert).
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -265,6 +259,7 @@ route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restric
   w4a16::cluster_arrive();
   w4a16::cluster_wait();
   // Four lanes per four logits, each lane the partials of RCS / 4 CTAs.
+  const uint32_t after = w4a16::after_cluster_wait();
   const uint32_t mine = nt > rank ? (nt - rank + RCS - 1) / RCS : 0u;
   for (uint32_t i = threadIdx.x >> 2; i < mine * e16 / 4; i += RTHREADS / 4) {
     const uint32_t q = i / (e16 / 4), e = 4 * (i - q * (e16 / 4));
@@ -273,7 +268,7 @@ route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restric
     for (uint32_t k = 0; k < ksub; ++k) {
       float4 p[RCS / 4];
 #pragma unroll
-      for (uint32_t r = 0; r < RCS / 4; ++r) p[r] = ld_cluster_f32x4(at + 4 * k * plane, r0 + r);
+      for (uint32_t r = 0; r < RCS / 4; ++r) p[r] = w4a16::ld_cluster_f32x4(at + 4 * k * plane, r0 + r, after);
 #pragma unroll
       for (uint32_t r = 0; r < RCS / 4; ++r) { v.x += p[r].x; v.y += p[r].y; v.z += p[r].z; v.w += p[r].w; }
     }

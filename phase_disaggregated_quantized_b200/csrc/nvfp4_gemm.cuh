@@ -37,6 +37,7 @@
 #include "epilogue.cuh"
 #include "nvfp4_quantize.cuh"
 #include "ptx.cuh"
+#include "w4a16_gemm.cuh"
 
 namespace nvq {
 namespace w4a4 {
@@ -57,6 +58,10 @@ constexpr uint32_t ACC1_COL = 128;            // accumulator 1 starts here (over
 constexpr uint32_t SF_COL0 = 384;
 constexpr uint32_t SF_SLOT_COLS = 48;         // one k-stage: 4 x (4 A + 8 B) columns
 constexpr uint32_t SF_SLOTS = 2;
+
+constexpr int MAX_SLICES = 8;                 // CTAs that split one tile's k-stages (EPI 3)
+constexpr int PART_STRIDE = BN + 4;           // floats of a partial row: 16-byte stores of 8 rows meet no bank twice
+static_assert(BM * PART_STRIDE * 4 <= STAGES * (A_BYTES + B_BYTES), "partial tile overlays the operand ring");
 
 constexpr int OFF_A = 0;
 constexpr int OFF_B = OFF_A + STAGES * A_BYTES;
@@ -90,8 +95,9 @@ struct Params {
   uint8_t* h_scales;       // tiled E4M3 scales of H, padded rows zero
   const float* t_h;        // static tensor scale of H
   uint32_t h_katoms;       // (N / 2) / 64
-  // Bias, activation, residual epilogue only (the residual comes through its own tensor map)
+  // Bias, activation, residual epilogues only (EPI 2: Y and the residual through tensor maps)
   EpiParams epi;
+  void* y;
 };
 
 // Tile order: the tiles in flight at once (one per SM) cover a band of tiles
@@ -218,6 +224,13 @@ __device__ __forceinline__ uint32_t acc_col(uint32_t buf) { return buf ? ACC1_CO
 // up, gate, up, ...); H = silu(gate) * up quantized to NVFP4 with a static t_h.
 // EPI 2: Y = BF16(act(alpha acc + bias) + residual), Y and the residual with
 // row strides of their own.
+// EPI 3: the same for no more tiles than SMs: the CTAs of a cluster split the k-stages
+// of one tile and then its rows.  Their partial sums meet in shared memory across the
+// cluster, in rank order.  There a tile has its SM to itself: a k-stage takes 0.8 to
+// 1.3 us (the loads of one SM), and the epilogue has no next tile to hide behind, so
+// more CTAs per tile shorten both (M 400, N 1000, K 8192: 32.1 us as EPI 2, 14.8 with
+// four CTAs; M 777, N 5128, K 1088: 15.9 and, with one, 14.2; M 3, N 1208, K 64: 10.1
+// and 6.3, there for the plain stores in place of TMA's).
 template <int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
 nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -258,7 +271,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     fence_mbar_init();
     prefetch_tensormap(&tmap_a);
     prefetch_tensormap(&tmap_b);
-    if (EPI != 1) prefetch_tensormap(&tmap_y);
+    if (EPI == 0 || EPI == 2) prefetch_tensormap(&tmap_y);
     if (EPI == 2 && p.epi.residual != nullptr) prefetch_tensormap(&tmap_r);
   }
   if (warp == 0) {
@@ -270,6 +283,26 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
   tc_fence_after();
   const uint32_t tmem_base = *tmem_ptr_smem;
   const uint32_t num_tiles = p.num_m_tiles * p.num_n_tiles;
+  // This CTA's tiles and k-stages (EPI 3: one tile per cluster, a slice of its stages per CTA).
+  const uint32_t first_tile = EPI == 3 ? w4a16::cluster_id() : blockIdx.x;
+  const uint32_t tile_step = EPI == 3 ? num_tiles : gridDim.x;
+  uint32_t ks0 = 0, ks1 = p.num_k_stages;
+  if constexpr (EPI == 3) {
+    const uint32_t slices = gridDim.x / num_tiles, rank = w4a16::cluster_rank();
+    ks0 = p.num_k_stages * rank / slices;
+    ks1 = p.num_k_stages * (rank + 1) / slices;
+  }
+  if constexpr (EPI >= 2) {
+    // Launched as a programmatic dependent: everything above overlapped the kernel
+    // before; the first weights are on their way into L2.
+    if (warp == 0 && lane == 0 && first_tile < num_tiles) {
+      uint32_t mt, nt;
+      tile_coords(first_tile, p, mt, nt);
+      for (uint32_t ks = ks0; ks < min(ks1, ks0 + STAGES); ++ks) tma_prefetch_2d(&tmap_b, (int)(ks * BKB), (int)(nt * BN));
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -278,11 +311,11 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       uint32_t stage = 0, phase = 0;
       uint32_t pending = 0, pending_parity = 0;               // per-stage bit masks
       bool ok = true;
-      for (uint32_t tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
+      for (uint32_t tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
         uint32_t mt, nt;
         tile_coords(tile, p, mt, nt);
         const uint32_t nb_atoms = min(2u, p.n_row_atoms - 2 * nt);
-        for (uint32_t ks = 0; ks < p.num_k_stages; ++ks) {
+        for (uint32_t ks = ks0; ks < ks1; ++ks) {
           if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1)) { ok = false; break; }
           const uint32_t natoms = min(4u, p.k_atoms - 4 * ks);
           // The scale atoms complete on a barrier of their own and go first, so
@@ -318,7 +351,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     uint32_t stage = 0, phase = 0, acc_par = 0, local = 0;
     uint32_t slot = 0, slot_phase = 0;
     bool ok = true;
-    for (uint32_t tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++local) {
+    for (uint32_t tile = first_tile; tile < num_tiles && ok; tile += tile_step, ++local) {
       const uint32_t buf = local & 1u;
       // This accumulator was drained (tile - 2), and the columns it shares with
       // the other accumulator were read for the previous tile.
@@ -327,7 +360,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
       if (local > 0 && !(ok = warp_mbar_wait(bar_overlap, (local - 1) & 1u))) break;
       tc_fence_after();
       const uint32_t d_tmem = tmem_base + acc_col(buf);
-      for (uint32_t ks = 0; ks < p.num_k_stages; ++ks) {
+      for (uint32_t ks = ks0; ks < ks1; ++ks) {
         if (!(ok = warp_mbar_wait(bar_full + 8 * stage, phase))) break;
         if (!(ok = warp_mbar_wait(bar_sf_full + 8 * slot, slot_phase))) break;
         tc_fence_after();
@@ -337,7 +370,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
           const uint32_t sf = tmem_base + SF_COL0 + SF_SLOT_COLS * slot;
           const uint32_t natoms = min(4u, p.k_atoms - 4 * ks);
           for (uint32_t j = 0; j < natoms; ++j)     // 32 bytes (64 FP4 elements) per k step
-            tc_mma_nvf4(d_tmem, ad + 2 * j, bd + 2 * j, IDESC, sf + 4 * j, sf + 16 + 8 * j, (ks | j) != 0u);
+            tc_mma_nvf4(d_tmem, ad + 2 * j, bd + 2 * j, IDESC, sf + 4 * j, sf + 16 + 8 * j, EPI == 3 ? (uint32_t)(ks != ks0 || j != 0u) : (uint32_t)((ks | j) != 0u));
           tc_commit(bar_empty + 8 * stage);                    // also frees this stage's scale slot
         }
         __syncwarp();
@@ -365,8 +398,8 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     // (so the MMA thread commits once per k-stage, for both).
     uint32_t lag_stage = 0, lag_phase = 0, kg = 0;
     bool ok = true;
-    for (uint32_t tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
-      for (uint32_t ks = 0; ks < p.num_k_stages; ++ks, ++kg) {
+    for (uint32_t tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
+      for (uint32_t ks = ks0; ks < ks1; ++ks, ++kg) {
         if (kg >= SF_SLOTS) {
           if (!(ok = warp_mbar_wait(bar_empty + 8 * lag_stage, lag_phase))) break;
           if (++lag_stage == STAGES) { lag_stage = 0; lag_phase ^= 1; }
@@ -477,6 +510,26 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
     (void)row;
+    } else if constexpr (EPI == 3) {
+      // alpha acc of this CTA's k-stages into the operand ring, which nothing uses any more.
+      uint32_t mt, nt;
+      tile_coords(first_tile, p, mt, nt);
+      if (ks0 < ks1 && mt * BM + q * 32 < p.M && warp_mbar_wait(bar_acc_full, 0)) {
+        tc_fence_after();
+        float* to = reinterpret_cast<float*>(smem) + row * PART_STRIDE + 128 * h;
+#pragma unroll 1
+        for (uint32_t ch = 0; ch < 2; ++ch) {
+          uint32_t v[64];
+          tc_ld_32x32b_x64(tmem_base + ((q * 32u) << 16) + 128 * h + C_COLS * ch, v);
+          tc_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            *reinterpret_cast<float4*>(to + C_COLS * ch + 4 * e) =
+                make_float4(__uint_as_float(v[4 * e]) * alpha, __uint_as_float(v[4 * e + 1]) * alpha,
+                            __uint_as_float(v[4 * e + 2]) * alpha, __uint_as_float(v[4 * e + 3]) * alpha);
+        }
+      }
+      __syncwarp();
     } else if constexpr (EPI == 2) {
     // As EPI 0, with each 32 x 64 chunk of the residual loaded by TMA into the
     // warp's staging buffer (where the result then replaces it): the tile's
@@ -662,6 +715,56 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+  if constexpr (EPI == 3) {
+    // Every rank finishes its share of the tile's rows: a warp a row at a time, a lane
+    // columns 4 lane .. and 128 + 4 lane .. of it.
+    w4a16::cluster_arrive();
+    w4a16::cluster_wait();
+    const uint32_t after = w4a16::after_cluster_wait();
+    uint32_t mt, nt;
+    tile_coords(first_tile, p, mt, nt);
+    const uint32_t slices = gridDim.x / num_tiles, slog = __ffs(slices) - 1, rank = w4a16::cluster_rank();   // a power of two
+    const uint32_t rows = min((uint32_t)BM, p.M - mt * BM), r1 = rows * (rank + 1) / slices;
+    const uint32_t col = nt * BN + 4 * lane;
+    const bool in[2] = {col < p.N, col + 128 < p.N};           // N % 8 == 0
+    uint2 bias[2] = {};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (p.epi.bias && in[j]) bias[j] = *reinterpret_cast<const uint2*>(p.epi.bias + col + 128 * j);
+#pragma unroll 2
+    for (uint32_t r = rows * rank / slices + warp; r < r1; r += THREADS / 32) {
+      const size_t m = mt * BM + r;
+      uint2 res[2] = {};
+      float v[2][4] = {};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (p.epi.residual && in[j]) res[j] = *reinterpret_cast<const uint2*>(p.epi.residual + m * p.epi.ldr + col + 128 * j);
+#pragma unroll 4
+      for (uint32_t k = 0; k < slices; ++k) {
+        if ((p.num_k_stages * (k + 1)) >> slog == (p.num_k_stages * k) >> slog) continue;   // a slice without a stage
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {                          // columns past N hold sums of nothing, inside the row
+          const float4 f = w4a16::ld_cluster_f32x4(sbase + (r * PART_STRIDE + 4 * lane + 128 * j) * 4, k, after);
+          v[j][0] += f.x; v[j][1] += f.y; v[j][2] += f.z; v[j][3] += f.w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[j][0] += bf16_lo(bias[j].x); v[j][1] += bf16_hi(bias[j].x); v[j][2] += bf16_lo(bias[j].y); v[j][3] += bf16_hi(bias[j].y);
+      }
+      float (&flat)[8] = reinterpret_cast<float (&)[8]>(v);
+      activate(flat, p.epi.act);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v[j][0] += bf16_lo(res[j].x); v[j][1] += bf16_hi(res[j].x); v[j][2] += bf16_lo(res[j].y); v[j][3] += bf16_hi(res[j].y);
+        if (in[j])
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + m * p.epi.ldy + col + 128 * j) =
+              make_uint2(pack_bf16x2(v[j][0], v[j][1]), pack_bf16x2(v[j][2], v[j][3]));
+      }
+    }
+    w4a16::cluster_arrive();                                  // nobody reads this CTA's sums any more
+    w4a16::cluster_wait();
   }
 }
 

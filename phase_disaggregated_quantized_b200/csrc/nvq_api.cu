@@ -148,6 +148,45 @@ nvq_status launch_w4a16(const void* x, const uint8_t* pc, const void* ps, void* 
   return launch_status("w4a16_kernel");
 }
 
+// Once per device and kernel: the opt-ins to more shared memory and to clusters of more than 8 CTAs.
+template <typename K>
+nvq_status kernel_opt_in(K kernel, int bytes, bool wide_cluster, std::once_flag (&once)[kMaxDevices],
+                         cudaError_t (&err)[kMaxDevices], const char* where) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  if (dev < 0 || dev >= kMaxDevices) return fail(NVQ_ERR_CUDA, "device index out of range");
+  std::call_once(once[dev], [&] {
+    err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err[dev] == cudaSuccess && wide_cluster)
+      err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  return err[dev] == cudaSuccess ? NVQ_OK : cuda_fail(err[dev], where);
+}
+
+// A launch that may begin during the preceding kernel's tail; `cluster` CTAs per cluster (0: none).
+template <typename... P, typename... A>
+nvq_status launch_dependent(const char* where, void (*kernel)(P...), int grid, int threads, size_t smem, int cluster,
+                            cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) return cuda_fail(e, where);
+  return launch_status(where);
+}
+
 // Workspace of nvq_linear's W4A4 path: activation codes, tiled scales, t and
 // the quantizer's scratch, each section 256-byte aligned.
 struct LinearWs {
@@ -481,12 +520,13 @@ namespace {
 
 // EPI 0: y_bf16 receives Y.  EPI 1: h_* receive NVFP4(silu(gate) * up) with the
 // static scale t_h (B rows interleaved in blocks of 128: gate, up, ...).  EPI 2:
-// y_bf16 receives act(Y + bias) + residual, row strides in epi.
+// y_bf16 receives act(Y + bias) + residual, row strides in epi.  EPI 3: the same,
+// `slices` CTAs per tile.
 template <int EPI>
 nvq_status launch_w4a4(const uint8_t* x_codes, const uint8_t* x_scales, const float* t_x, const uint8_t* w_codes,
                        const uint8_t* w_scales, const float* t_w, void* y_bf16, int64_t M, int64_t N, int64_t K,
                        uint8_t* h_codes, uint8_t* h_scales, const float* t_h, cudaStream_t stream,
-                       const nvq::EpiParams& epi = {}) {
+                       const nvq::EpiParams& epi = {}, int slices = 1) {
   using namespace nvq::w4a4;
   CUtensorMap ma, mb, my, mr;
   memset(&my, 0, sizeof(my));                               // EPI 1 never touches Y
@@ -496,7 +536,7 @@ nvq_status launch_w4a4(const uint8_t* x_codes, const uint8_t* x_scales, const fl
                    BKB, BM) ||
       !make_map_2d(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, (uint64_t)K / 2, (uint64_t)N, (uint64_t)K / 2,
                    BKB, BN) ||
-      (EPI != 1 && !make_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y_bf16, (uint64_t)N, (uint64_t)M,
+      ((EPI == 0 || EPI == 2) && !make_map_2d(&my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y_bf16, (uint64_t)N, (uint64_t)M,
                                 ldy * 2, C_COLS, 32)) ||         // one epilogue warp: 32 rows x 64 columns
       (EPI == 2 && epi.residual != nullptr &&
        !make_map_2d(&mr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, epi.residual, (uint64_t)N, (uint64_t)M,
@@ -522,22 +562,29 @@ nvq_status launch_w4a4(const uint8_t* x_codes, const uint8_t* x_scales, const fl
   p.t_h = t_h;
   p.h_katoms = (uint32_t)(N / 2 / 64);
   p.epi = epi;
-  // The shared-memory opt-in is a per-device setting of the kernel: once per device.
-  int dev = 0;
-  const cudaError_t de = cudaGetDevice(&dev);
-  if (de != cudaSuccess) return cuda_fail(de, "nvfp4_gemm_w4a4: cudaGetDevice");
-  if (dev < 0 || dev >= kMaxDevices) return fail(NVQ_ERR_CUDA, "nvfp4_gemm_w4a4: device index out of range");
+  p.y = y_bf16;
+  (void)slices;
   static std::once_flag once[kMaxDevices];
   static cudaError_t attr_err[kMaxDevices];   // zero = cudaSuccess
-  std::call_once(once[dev], [dev] {
-    attr_err[dev] = cudaFuncSetAttribute(nvfp4_gemm_kernel<EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         SMEM_BYTES);
-  });
-  if (attr_err[dev] != cudaSuccess) return cuda_fail(attr_err[dev], "nvfp4_gemm_w4a4: smem attribute");
+  const nvq_status st = kernel_opt_in(nvfp4_gemm_kernel<EPI>, SMEM_BYTES, false, once, attr_err, "nvfp4_gemm_w4a4: smem attribute");
+  if (st != NVQ_OK) return st;
   const uint64_t tiles = (uint64_t)p.num_m_tiles * p.num_n_tiles;
+  if constexpr (EPI == 3)
+    return launch_dependent("nvfp4_gemm_kernel", nvfp4_gemm_kernel<EPI>, (int)tiles * slices, THREADS, SMEM_BYTES, slices, stream,
+                            ma, mb, my, mr, p);
   const int grid = (int)std::min<uint64_t>(tiles, (uint64_t)sm_count());
+  if constexpr (EPI == 2)
+    return launch_dependent("nvfp4_gemm_kernel", nvfp4_gemm_kernel<EPI>, grid, THREADS, SMEM_BYTES, 0, stream, ma, mb, my, mr, p);
   nvfp4_gemm_kernel<EPI><<<grid, THREADS, SMEM_BYTES, stream>>>(ma, mb, my, mr, p);
   return launch_status("nvfp4_gemm_kernel");
+}
+
+// CTAs per tile for a product with an epilogue: as many of a cluster as the device
+// holds for all tiles at once (measured on a B200 with one CTA per SM: 15 clusters of
+// 8, 33 of 4, 74 of 2); 0: more tiles than SMs, for which the persistent kernel is made.
+int w4a4_slices(int64_t M, int64_t N) {
+  const int64_t tiles = ((M + nvq::w4a4::BM - 1) / nvq::w4a4::BM) * ((N + nvq::w4a4::BN - 1) / nvq::w4a4::BN);
+  return tiles <= 15 ? 8 : tiles <= 33 ? 4 : tiles <= 74 ? 2 : tiles <= sm_count() ? 1 : 0;
 }
 
 }  // namespace
@@ -601,6 +648,10 @@ nvq_status nvfp4_gemm_w4a4_epilogue(const uint8_t* x_codes, const uint8_t* x_sca
   nvq::EpiParams ep;
   const nvq_status st = epilogue_params("nvfp4_gemm_w4a4_epilogue", epilogue, y_bf16, M, N, &ep);
   if (st != NVQ_OK) return st;
+  const int slices = w4a4_slices(M, N);
+  if (slices > 0)
+    return launch_w4a4<3>(x_codes, x_scales, t_x, w_codes, w_scales, t_w, y_bf16, M, N, K, nullptr, nullptr, nullptr,
+                          stream, ep, slices);
   return launch_w4a4<2>(x_codes, x_scales, t_x, w_codes, w_scales, t_w, y_bf16, M, N, K, nullptr, nullptr, nullptr,
                         stream, ep);
 }
@@ -755,45 +806,6 @@ MoeWs moe_ws_layout(int64_t T, int64_t H, int64_t I, int64_t topk) {
   W.logits = W.partial + align256((size_t)2 * kMoeMaxGrid * tc * 32 * 4);
   W.total = W.logits + (size_t)kMoeMaxGrid * 16 * tc * 4;   // at most one 16-expert tile per CTA
   return W;
-}
-
-// Once per device and kernel: the opt-ins to more shared memory and to clusters of more than 8 CTAs.
-template <typename K>
-nvq_status kernel_opt_in(K kernel, int bytes, bool wide_cluster, std::once_flag (&once)[kMaxDevices],
-                         cudaError_t (&err)[kMaxDevices], const char* where) {
-  int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, where);
-  if (dev < 0 || dev >= kMaxDevices) return fail(NVQ_ERR_CUDA, "device index out of range");
-  std::call_once(once[dev], [&] {
-    err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (err[dev] == cudaSuccess && wide_cluster)
-      err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  });
-  return err[dev] == cudaSuccess ? NVQ_OK : cuda_fail(err[dev], where);
-}
-
-// A launch that may begin during the preceding kernel's tail; `cluster` CTAs per cluster (0: none).
-template <typename... P, typename... A>
-nvq_status launch_dependent(const char* where, void (*kernel)(P...), int grid, int threads, size_t smem, int cluster,
-                            cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3((unsigned)threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) return cuda_fail(e, where);
-  return launch_status(where);
 }
 
 nvq_status route_validate(const char* name, const void* x, const void* wr, int64_t T, int64_t E, int64_t H, int topk,

@@ -110,6 +110,20 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
+// 16 bytes of the shared memory of CTA `rank` of the cluster.  The load may be moved
+// freely among others; `after` (after_cluster_wait) keeps it behind the barrier that
+// made the data visible.
+__device__ __forceinline__ uint32_t after_cluster_wait() {
+  uint32_t zero;
+  asm volatile("mov.u32 %0, 0;" : "=r"(zero) :: "memory");
+  return zero;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t saddr, uint32_t rank, uint32_t after) {
+  float4 v;
+  asm("{ .reg .b32 a; mapa.shared::cluster.u32 a, %4, %5; ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [a]; }"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(saddr + after), "r"(rank));
+  return v;
+}
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }

@@ -85,7 +85,9 @@ def _cu(t):
 INT4_SHAPES = [(1, 32, 128), (1, 4096, 256), (7, 96, 384), (8, 2080, 1152), (9, 64, 128), (16, 352, 4096),
                (17, 32, 256), (32, 1056, 384), (33, 96, 128), (70, 64, 640)]
 NVFP4_SHAPES = [(1, 8, 64), (5, 264, 128), (31, 72, 192), (128, 256, 256), (129, 520, 1088), (300, 1000, 320),
-                (1030, 2312, 64)]
+                (1030, 2312, 64),
+                # few tiles, whose k-stages 8, 4 or 2 CTAs split
+                (5, 264, 2112), (1, 8, 4096), (129, 1032, 2048), (300, 2312, 832), (257, 3600, 768), (40, 16, 704)]
 SHAPES = [(Int4, s) for s in INT4_SHAPES] + [(Nvfp4, s) for s in NVFP4_SHAPES]
 
 
