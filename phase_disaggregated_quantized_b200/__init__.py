@@ -489,8 +489,7 @@ def w4a16_moe_experts(x, ids, weights, gate_up, down, E: int, I: int, *, residua
 
 def w4a16_moe(x, w_router, gate_up, down, I: int, topk: int, *, renormalize: bool = True, residual=None, ids=None,
               weights=None, y=None, workspace=None, stream=None):
-    """The whole layer: what moe_route and then w4a16_moe_experts compute, in one
-    launch per 32 tokens.  Returns (y, ids, weights)."""
+    """The whole layer: moe_route, then w4a16_moe_experts, in one call.  Returns (y, ids, weights)."""
     return _call("w4a16_moe", stream, x, x, w_router, gate_up, down, I, topk, renormalize, residual, ids,
                  weights, y, workspace)
 

@@ -6,20 +6,20 @@
 //   h[t, j]      = silu(Wg[e] x[t]) * (Wu[e] x[t]),   e = ids[t, j]
 //   y[t]         = residual[t] + sum_j Wd[e] (w[t, j] h[t, j])
 //
-// The router alone is one cluster of CTAs; the experts, with or without the
-// router before them, are one cooperative launch: a CTA per SM, phases apart by
-// grid barriers (router | selection, gate and up | down).  The experts are in the
-// packed form of the decode GEMM (units of 32 rows x 128 k), gate and up rows in
-// turn by 16, so that one unit holds 16 gate rows (MMA tile 0) and the matching
-// 16 up rows (tile 1) and a lane has both halves of its h.  Weights are read from
-// memory once per expert and eight of its tokens; which experts those are is
-// known only on the device, so each CTA first sorts the (token, choice) pairs by
-// expert into segments of at most eight tokens (one MMA column each).
+// Three launches chained by programmatic dependent launch: the router, gate and
+// up, down.  (One cooperative launch with grid barriers between the phases was
+// slower for few tokens, 12.3 against 10.0 us for 1344 units of weights, and 5%
+// faster for the largest batches: a grid barrier takes 1.8 us and the gap before a
+// cooperative launch 2.6, a dependent launch 0.75.)  The experts are in the packed
+// form of the decode GEMM (units of 32 rows x 128 k), gate and up rows in turn by
+// 16, so that one unit holds 16 gate rows (MMA tile 0) and the matching 16 up rows
+// (tile 1) and a lane has both halves of its h.  Weights are read from memory once
+// per expert and eight of its tokens; which experts those are is known only on the
+// device, so each CTA first sorts the (token, choice) pairs by expert into segments
+// of at most eight tokens (one MMA column each).
 #pragma once
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <type_traits>
-#include <utility>
 #include "epilogue.cuh"
 #include "ptx.cuh"
 #include "w4a16_gemm.cuh"
@@ -300,7 +300,7 @@ route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restric
 }
 
 // ------------------------------------------------------------------ segments
-constexpr int EWARPS = 16;
+constexpr int EWARPS = 8;
 constexpr int ETHREADS = EWARPS * 32;
 constexpr uint32_t COLS = 8;        // tokens of one segment
 
@@ -320,8 +320,8 @@ struct FastDiv {
 
 struct ExpertParams {
   const __nv_bfloat16* x;           // [T, H]
-  int32_t* ids;                     // [T, topk]: read, or written by the router phase
-  float* weights;                   // [T, topk]
+  const int32_t* ids;               // [T, topk]
+  const float* weights;             // [T, topk]
   const uint8_t* gu_codes;          // E x [2I, H] packed
   const uint8_t* gu_scales;
   const uint8_t* d_codes;           // E x [H, I] packed
@@ -333,11 +333,7 @@ struct ExpertParams {
   float* partial;                   // [2 gridDim][T][32]
   uint32_t T, E, H, I, topk;
   uint32_t stage;                   // all of h fits in shared memory
-  FastDiv by_topk, by_grid, by_g, by_rtiles, by_gi;   // topk, gridDim, H / 128, I / 16, I / 128
-  // the router phase
-  const __nv_bfloat16* wr;          // [E, H]
-  float* logits;                    // [slices][T][16 etiles] partial sums
-  uint32_t renorm, etiles, slices;
+  FastDiv by_topk, by_grid, by_g, by_rtiles, by_gi;   // topk, gridDim of both kernels, H / 128, I / 16, I / 128
 };
 
 struct Plan {
@@ -364,13 +360,13 @@ struct DownCut {
 // Sorts the pairs of pl.id / pl.w by expert into segments of at most COLS tokens
 // of one expert.  An id outside [0, E) is no choice; an expert that a token names
 // twice counts once, with the sum of the weights (the same sum of products), so
-// that a segment never holds a token twice.  Called by the whole CTA, pl.id and
-// pl.w filled and visible.
+// that a segment never holds a token twice.  Called by the whole CTA.
 __device__ __forceinline__ void build_plan(Plan& pl, const ExpertParams& p) {
   const uint32_t P = p.T * p.topk, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
   if (P <= 32) {                    // one warp, a pair per lane; experts in the order of their first pair
     if (warp == 0) {
-      const int32_t id = lane < P ? pl.id[lane] : -1;
+      const int32_t id = lane < P ? p.ids[lane] : -1;
+      const float w = lane < P ? p.weights[lane] : 0.f;
       const uint32_t t = p.by_topk.div(lane);
       const bool valid = lane < P && (uint32_t)id < p.E;
       const uint32_t lt = (1u << lane) - 1u;
@@ -378,9 +374,13 @@ __device__ __forceinline__ void build_plan(Plan& pl, const ExpertParams& p) {
       const uint32_t ends = (t + 1) * p.topk;                          // the token's lanes [t topk, ends)
       const uint32_t own = same & (ends >= 32 ? 0xFFFFFFFFu : (1u << ends) - 1u) & ~((1u << (t * p.topk)) - 1u);
       const bool first = valid && (own & lt) == 0;
-      float s = lane < P ? pl.w[lane] : 0.f;
-      if (first)
-        for (uint32_t m = own & ~lt & ~(1u << lane); m; m &= m - 1) s += pl.w[__ffs(m) - 1];
+      float s = w;
+      const uint32_t again = first ? own & ~lt & ~(1u << lane) : 0u;   // further mentions by the same token
+      if (__any_sync(0xFFFFFFFFu, again != 0u))
+        for (uint32_t q = 0; q < P; ++q) {
+          const float other = __shfl_sync(0xFFFFFFFFu, w, q);
+          if ((again >> q) & 1u) s += other;
+        }
       const uint32_t group = same & __ballot_sync(0xFFFFFFFFu, first);  // the expert's pairs that count
       const uint32_t n = __popc(group), within = __popc(group & lt);
       const bool leads = first && within == 0;
@@ -410,24 +410,34 @@ __device__ __forceinline__ void build_plan(Plan& pl, const ExpertParams& p) {
     __syncthreads();
     return;
   }
-  static_assert(kMaxExperts == ETHREADS && kMaxPairs == ETHREADS, "an expert and a pair per thread");
+  for (uint32_t i = tid; i < P; i += ETHREADS) {
+    pl.id[i] = p.ids[i];
+    pl.w[i] = p.weights[i];
+  }
+  static_assert(kMaxExperts == 2 * ETHREADS && kMaxPairs == 2 * ETHREADS, "two experts and two pairs per thread");
   pl.mask[tid] = 0u;
+  pl.mask[tid + ETHREADS] = 0u;
   __syncthreads();
-  const uint32_t t = p.by_topk.div(tid), j0 = t * p.topk;
-  const int32_t id = tid < P ? pl.id[tid] : -1;
-  bool first = (uint32_t)id < p.E;
-  if (first) {
-    float s = pl.w[tid];
+  bool first[2];
+#pragma unroll
+  for (uint32_t k = 0; k < 2; ++k) {
+    const uint32_t i = tid + k * ETHREADS, t = p.by_topk.div(i), j0 = t * p.topk;
+    const int32_t id = i < P ? pl.id[i] : -1;
+    first[k] = (uint32_t)id < p.E;
+    if (first[k]) {
+      float s = pl.w[i];
 #pragma unroll 4
-    for (uint32_t j = j0; j < tid; ++j) first &= pl.id[j] != id;
+      for (uint32_t j = j0; j < i; ++j) first[k] &= pl.id[j] != id;
 #pragma unroll 4
-    for (uint32_t j = tid + 1; j < j0 + p.topk; ++j)
-      if (pl.id[j] == id) s += pl.w[j];
-    pl.pw[tid] = s;
-    if (first) atomicOr(&pl.mask[id], 1u << t);
+      for (uint32_t j = i + 1; j < j0 + p.topk; ++j)
+        if (pl.id[j] == id) s += pl.w[j];
+      pl.pw[i] = s;
+      if (first[k]) atomicOr(&pl.mask[id], 1u << t);
+    }
   }
   __syncthreads();
-  const uint32_t n = __popc(pl.mask[tid]), add = n | ((n + COLS - 1) / COLS) << 16;
+  const uint32_t n0 = __popc(pl.mask[2 * tid]), n1 = __popc(pl.mask[2 * tid + 1]);
+  const uint32_t add = (n0 + n1) | ((n0 + COLS - 1) / COLS + (n1 + COLS - 1) / COLS) << 16;
   uint32_t inc = add;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -438,21 +448,28 @@ __device__ __forceinline__ void build_plan(Plan& pl, const ExpertParams& p) {
   __syncthreads();
   uint32_t before = inc - add;
   for (uint32_t w = 0; w < warp; ++w) before += pl.warp_sum[w];
-  const uint32_t slot = before & 0xFFFFu;
-  uint32_t seg = before >> 16;
-  pl.first[tid] = (uint16_t)slot;
-  for (uint32_t q = 0; q < n; q += COLS, ++seg) {
-    pl.seg_e[seg] = (uint16_t)tid;
-    pl.seg_s[seg] = (uint16_t)(slot + q);
-    pl.seg_n[seg] = (uint8_t)min(COLS, n - q);
+  uint32_t slot = before & 0xFFFFu, seg = before >> 16;
+#pragma unroll
+  for (uint32_t k = 0; k < 2; ++k) {
+    const uint32_t n = k ? n1 : n0;
+    pl.first[2 * tid + k] = (uint16_t)slot;
+    for (uint32_t q = 0; q < n; q += COLS, ++seg) {
+      pl.seg_e[seg] = (uint16_t)(2 * tid + k);
+      pl.seg_s[seg] = (uint16_t)(slot + q);
+      pl.seg_n[seg] = (uint8_t)min(COLS, n - q);
+    }
+    slot += n;
   }
   if (tid == ETHREADS - 1) pl.segments = seg;
   __syncthreads();
-  if (first) {
-    const uint32_t k = pl.first[id] + __popc(pl.mask[id] & ((1u << t) - 1u));
-    pl.pair[k] = (uint16_t)tid;
-    pl.token[k] = (uint8_t)t;
-  }
+#pragma unroll
+  for (uint32_t k = 0; k < 2; ++k)
+    if (first[k]) {
+      const uint32_t i = tid + k * ETHREADS, t = p.by_topk.div(i);
+      const uint32_t at = pl.first[pl.id[i]] + __popc(pl.mask[pl.id[i]] & ((1u << t) - 1u));
+      pl.pair[at] = (uint16_t)i;
+      pl.token[at] = (uint8_t)t;
+    }
   __syncthreads();
 }
 
@@ -620,30 +637,31 @@ __device__ __forceinline__ uint32_t ticket(uint32_t* counter) {
 // ------------------------------------------------------------------ the layer
 constexpr int RING = 3;
 constexpr int RING_BYTES = EWARPS * RING * SLOT;
-// Behind the ring: the down phase's per-token rows of each warp, before that the
-// gate and up phase's cut tiles (two of 16 x 8 x 2 sums per warp).
-// All of h (P pairs of I values, two halves each) goes there too when it fits
-// beside the rows of a call with the most tokens: a few tokens' h, which every
-// CTA reads whole.
-constexpr int kBehindRing = EWARPS * kMaxTokens * 32 * 4;
-constexpr bool stage_h(int64_t T, int64_t P, int64_t I) { return EWARPS * T * 32 * 4 + P * I * 4 <= kBehindRing; }
-// The gate and up phase keeps there the column offsets of up to kOffsets (segment,
-// group) pairs behind the cut tiles.
+// Shared memory behind the ring.  Gate and up: the cut tiles (two of 16 x 8 x 2 sums
+// per warp) and the column offsets of up to kOffsets (segment, group) pairs.  Down: the
+// per-token rows of each warp and, where it fits within kBehindRing with them, all of h
+// (P pairs of I values, two halves each): a few tokens' h, which every CTA reads whole.
+// Both kernels fit on an SM twice, or once each.
 constexpr uint32_t kOffsets = 512;
 constexpr int kCutTiles = EWARPS * 2 * 1024;
-constexpr int layer_smem(int64_t T, int64_t P, int64_t I) {
-  const int64_t rows = EWARPS * T * 32 * 4 + (stage_h(T, P, I) ? P * I * 4 : 0), gate = kCutTiles + kOffsets * 32;
-  return RING_BYTES + (int)(rows > gate ? rows : gate);
+constexpr int kGateUpSmem = RING_BYTES + kCutTiles + (int)kOffsets * 32;
+constexpr int kBehindRing = 40 * 1024;
+constexpr bool stage_h(int64_t T, int64_t P, int64_t I) { return EWARPS * T * 32 * 4 + P * I * 4 <= kBehindRing; }
+constexpr int down_smem(int64_t T, int64_t P, int64_t I) {
+  return RING_BYTES + (int)(EWARPS * T * 32 * 4 + (stage_h(T, P, I) ? P * I * 4 : 0));
 }
+static_assert(EWARPS * kMaxTokens * 32 * 4 <= kBehindRing, "the rows of the most tokens");
+static_assert(2 * (kGateUpSmem + sizeof(Plan) + 1024) <= 228 * 1024 && 2 * (RING_BYTES + kBehindRing + sizeof(Plan) + 1024) <= 228 * 1024,
+              "two CTAs per SM");
 
-// Down: a round (one unit per warp) takes about 1 us, 0.6 us for one row tile of the
-// unit; joining cut tiles through memory takes about 2.5 us.  So: half tiles (16 columns)
+// Down: a round (one unit per warp) takes about 0.6 us, 0.4 us for one row tile of the
+// unit; joining cut tiles through memory takes about 2.5 us, four rounds.  So: half tiles (16 columns)
 // where that leaves no more of them than CTAs and is not slower, whole tiles, or even
 // parts of the flat sequence of units.
 __device__ __forceinline__ DownCut cut_down(const ExpertParams& p, uint32_t segments, uint32_t ntile, uint32_t Gi) {
   DownCut d;
   const uint32_t U = segments * Gi, total = U * ntile, grid = gridDim.x;
-  const uint32_t rounds = (U + EWARPS - 1) / EWARPS, joined = p.by_grid.div(total / EWARPS) + 3;
+  const uint32_t rounds = (U + EWARPS - 1) / EWARPS, joined = p.by_grid.div(total / EWARPS) + 5;
   d.half = 2 * ntile <= grid && rounds * 5 <= joined * 8;
   d.whole = d.half || p.by_grid.div(ntile + grid - 1) * rounds <= joined;
   const uint32_t pieces = d.whole ? (d.half ? 2 * ntile : ntile) : total;
@@ -662,114 +680,21 @@ __device__ __forceinline__ DownCut cut_down(const ExpertParams& p, uint32_t segm
   return d;
 }
 
-// One 64-wide k block of the router: 16 experts x 8 M tokens, K permuted alike in
-// both operands so that a lane's words are 32 consecutive bytes.
-template <int M>
-__device__ __forceinline__ void route_block(const uint4* lo, const uint4* hi, const uint4* const (&xb)[M], uint32_t ntile,
-                                            float (&acc)[M][4]) {
-  const uint4 l0 = __ldg(lo), l1 = __ldg(lo + 1), h0 = __ldg(hi), h1 = __ldg(hi + 1);
-  const uint32_t f[4][4] = {{l0.x, h0.x, l0.y, h0.y}, {l0.z, h0.z, l0.w, h0.w},
-                            {l1.x, h1.x, l1.y, h1.y}, {l1.z, h1.z, l1.w, h1.w}};
-#pragma unroll
-  for (int m = 0; m < M; ++m)
-    if ((uint32_t)m < ntile) {
-      const uint4 q0 = __ldg(xb[m]), q1 = __ldg(xb[m] + 1);
-      float d[4][4];
-      w4a16::mma_z(d[0], f[0], q0.x, q0.y);
-      w4a16::mma_z(d[1], f[1], q0.z, q0.w);
-      w4a16::mma_z(d[2], f[2], q1.x, q1.y);
-      w4a16::mma_z(d[3], f[3], q1.z, q1.w);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[m][e] += (d[0][e] + d[1][e]) + (d[2][e] + d[3][e]);
-    }
-}
-
 // Gate and up: a tile is one segment x 16 h columns (one packed row tile: 16 gate
 // and 16 up rows), H / 128 units.  A CTA owns whole tiles (segment-major, so that
 // it stays with one expert's rows of x), its warps equal runs of their units; a
 // tile inside one run is finished in registers, the others through shared memory.
-//
-// Down: a tile is 32 columns of y, all segments x I / 128 units.  With few units
-// a CTA takes whole tiles; else the flat sequence of units is cut into equal
-// parts, one per CTA.  A warp adds its run's products per token in its own
-// shared-memory rows, the warps' rows are added in order.  A tile that several
-// parts share is finished by the CTA that comes last (a ticket per tile), which
-// adds the parts' sums in order: nothing waits, and the result does not depend on
-// who came last.
-template <bool ROUTE>
-__global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) {
+__global__ void __launch_bounds__(ETHREADS, 2) gate_up_kernel(const ExpertParams p) {
   extern __shared__ __align__(16) uint8_t esm[];
   __shared__ Plan pl;
-  __shared__ DownCut cd;
-  __shared__ uint32_t last[2];
-  const auto grid = cooperative_groups::this_grid();
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g8 = lane >> 2, c = lane & 3u;
-  const uint32_t T = p.T, H = p.H, I = p.I, P = T * p.topk;
-
-  // ---- router: one CTA per 16 experts and slice of K, its warps side by side over the slice
-  if constexpr (ROUTE) {
-    float* part = reinterpret_cast<float*>(esm);                       // [EWARPS][8 ntile][16]
-    const uint32_t ntile = (T + 7) / 8, e16 = p.etiles * 16, nblk = H / 64;
-    for (uint32_t item = blockIdx.x; item < p.etiles * p.slices; item += gridDim.x) {
-      const uint32_t sl = item / p.etiles, et = item - sl * p.etiles;
-      const uint32_t s0 = nblk * sl / p.slices, s1 = nblk * (sl + 1) / p.slices;
-      const uint32_t k0 = s0 + (s1 - s0) * warp / EWARPS, k1 = s0 + (s1 - s0) * (warp + 1) / EWARPS;
-      const uint32_t r_lo = min(et * 16 + g8, p.E - 1), r_hi = min(et * 16 + g8 + 8, p.E - 1);   // rows past E: never selected
-      const uint4* lo = reinterpret_cast<const uint4*>(p.wr + (size_t)r_lo * H + 16 * c);
-      const uint4* hi = reinterpret_cast<const uint4*>(p.wr + (size_t)r_hi * H + 16 * c);
-      const uint4* xb[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) xb[m] = reinterpret_cast<const uint4*>(p.x + (size_t)min(8u * m + g8, T - 1) * H + 16 * c) + 8 * k0;
-      float acc[4][4] = {};
-#pragma unroll 2
-      for (uint32_t b = k0; b < k1; ++b) {
-        route_block<4>(lo + 8 * b, hi + 8 * b, xb, ntile, acc);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) xb[m] += 8;
-      }
-      float* q = part + warp * ntile * 128 + g8;
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        if ((uint32_t)m < ntile)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) q[(8 * m + 2 * c + (e & 1)) * 16 + (e & 2) * 4] = acc[m][e];
-      __syncthreads();
-      for (uint32_t i = threadIdx.x; i < T * 16; i += ETHREADS) {
-        float v = 0.f;
-#pragma unroll
-        for (uint32_t w = 0; w < EWARPS; ++w) v += part[w * ntile * 128 + i];
-        __stcg(p.logits + ((size_t)sl * T + (i >> 4)) * e16 + et * 16 + (i & 15u), v);
-      }
-      __syncthreads();
-    }
-    grid.sync();
-    // Every CTA selects for all tokens; one CTA per token writes the result.
-    for (uint32_t t = warp; t < T; t += EWARPS) {
-      uint32_t id;
-      float w;
-      select_experts(p.logits + (size_t)t * e16, p.slices, (size_t)T * e16, [](const float* q) { return __ldcg(q); },
-                     p.E, p.topk, p.renorm != 0, lane, id, w);
-      if (lane < p.topk) {
-        pl.id[t * p.topk + lane] = (int32_t)id;
-        pl.w[t * p.topk + lane] = w;
-        if (blockIdx.x == t % gridDim.x) {
-          p.ids[t * p.topk + lane] = (int32_t)id;
-          p.weights[t * p.topk + lane] = w;
-        }
-      }
-    }
-  } else {
-    for (uint32_t i = threadIdx.x; i < P; i += ETHREADS) {
-      pl.id[i] = p.ids[i];
-      pl.w[i] = p.weights[i];
-    }
-  }
-  __syncthreads();
+  const uint32_t H = p.H, I = p.I, P = p.T * p.topk;
+  grid_dependency_wait();
+  grid_launch_dependents();
   build_plan(pl, p);
-  const uint32_t segments = pl.segments, G = H / 128, rtiles = I / 16, Gi = I / 128, ntile = H / 32;
+  const uint32_t segments = pl.segments, G = H / 128, rtiles = I / 16;
   const size_t low = (size_t)P * I;                                    // from a high half of h to its low half
-
-  // ---- gate and up
+  for (uint32_t i = blockIdx.x * ETHREADS + threadIdx.x; i < H / 32; i += gridDim.x * ETHREADS) p.tickets[i] = 0u;
   Ring<RING> ring;
   ring.init(esm, warp, lane);
   {
@@ -859,12 +784,8 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
 #pragma unroll
       for (int i = 0; i < 4; ++i) b[i] = __ldg(row + at * 16 + i);
     };
-    // While the first weights are on their way: how the down phase is cut, and the
-    // column offsets of this CTA's segments, which each of their row tiles needs again.
-    if (warp == EWARPS - 1) {
-      const DownCut d = cut_down(p, segments, ntile, Gi);
-      if (lane == 0) cd = d;
-    }
+    // While the first weights are on their way: the column offsets of this CTA's
+    // segments, which each of their row tiles needs again.
     const uint32_t seg0 = p.by_rtiles.div(T0), nseg = mine ? p.by_rtiles.div(T0 + mine - 1) - seg0 + 1 : 0u;
     const bool given = nseg * G <= kOffsets;
     float2* offsets = reinterpret_cast<float2*>(esm + RING_BYTES + kCutTiles);   // [segment][group][c]
@@ -942,13 +863,32 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
       finish(acc, seg, tile - seg * rtiles);
     }
   }
+}
 
-  // ---- down
-  for (uint32_t i = blockIdx.x * ETHREADS + threadIdx.x; i < ntile; i += gridDim.x * ETHREADS) p.tickets[i] = 0u;
-  auto arrived = grid.barrier_arrive();                                // this CTA's h is written
+// Down: a tile is 32 columns of y, all segments x I / 128 units.  With few units a
+// CTA takes whole tiles or halves of them; else the flat sequence of units is cut into
+// equal parts, one per CTA.  A warp adds its run's products per token in its own
+// shared-memory rows, the warps' rows are added in order.  A tile that several parts
+// share is finished by the CTA that comes last (a ticket per tile), which adds the
+// parts' sums in order: nothing waits, and the result does not depend on who came last.
+__global__ void __launch_bounds__(ETHREADS, 2) down_kernel(const ExpertParams p) {
+  extern __shared__ __align__(16) uint8_t esm[];
+  __shared__ Plan pl;
+  __shared__ uint32_t last[2];
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g8 = lane >> 2, c = lane & 3u;
+  const uint32_t T = p.T, H = p.H, I = p.I, P = T * p.topk, Gi = I / 128, ntile = H / 32;
+  grid_launch_dependents();
+  // This kernel is launched when every CTA of the gate and up kernel is past its own
+  // wait, so ids and weights are final: the plan, the cut and the first weights do not
+  // wait for h.
+  build_plan(pl, p);
+  const uint32_t segments = pl.segments;
+  const size_t low = (size_t)P * I;                                    // from a high half of h to its low half
+  const DownCut cd = cut_down(p, segments, ntile, Gi);
+  Ring<RING> ring;
   const uint32_t U = segments * Gi;
   if (segments == 0) {                                                 // no token has an expert
-    grid.barrier_wait(std::move(arrived));
+    grid_dependency_wait();
     for (size_t i = (size_t)blockIdx.x * ETHREADS + threadIdx.x; i < (size_t)T * H; i += (size_t)gridDim.x * ETHREADS)
       p.y[i] = p.residual ? p.residual[i] : __float2bfloat16_rn(0.f);
     return;
@@ -1018,7 +958,7 @@ __global__ void __launch_bounds__(ETHREADS, 1) moe_kernel(const ExpertParams p) 
     clear_rows();
     if (F0 <= n0 * U && F1 >= n0 * U + U) residual_of(n0, res);
   }
-  grid.barrier_wait(std::move(arrived));
+  grid_dependency_wait();
 
   const __nv_bfloat16* h = p.h;
   if (p.stage) {                                                       // all of h fits behind the rows

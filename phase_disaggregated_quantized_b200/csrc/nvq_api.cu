@@ -788,14 +788,14 @@ nvq_status w4a16_sparse24_gemm(const void* x_bf16, const uint8_t* packed, const 
 // ------------------------------------------------------------------ mixture of experts
 namespace {
 
-// CTAs of the expert kernel: one on each of a B200's SMs.  A constant, so that the
+// CTAs of the expert kernels: two on each of a B200's SMs.  A constant, so that the
 // workspace (two partial tiles per CTA) can be sized without a device.
-constexpr int kMoeMaxGrid = 148;
+constexpr int kMoeMaxGrid = 2 * 148;
 // H and I, and one expert's down matrix: units of 512 segments are counted in 31 bits.
 constexpr int64_t kMoeMaxDim = (int64_t)1 << 20, kMoeMaxWeight = (int64_t)1 << 33;
 
 struct MoeWs {
-  size_t h, tickets, partial, logits, total;
+  size_t h, tickets, partial, total;
 };
 MoeWs moe_ws_layout(int64_t T, int64_t H, int64_t I, int64_t topk) {
   const size_t tc = (size_t)std::min<int64_t>(T, nvq::moe::kMaxTokens);
@@ -803,8 +803,7 @@ MoeWs moe_ws_layout(int64_t T, int64_t H, int64_t I, int64_t topk) {
   W.h = 0;
   W.tickets = align256(tc * (size_t)topk * (size_t)I * 4);
   W.partial = W.tickets + align256((size_t)(H / 32) * 4);
-  W.logits = W.partial + align256((size_t)2 * kMoeMaxGrid * tc * 32 * 4);
-  W.total = W.logits + (size_t)kMoeMaxGrid * 16 * tc * 4;   // at most one 16-expert tile per CTA
+  W.total = W.partial + (size_t)2 * kMoeMaxGrid * tc * 32 * 4;
   return W;
 }
 
@@ -879,54 +878,48 @@ nvq_status launch_route(const void* x, const void* wr, int64_t T, int64_t E, int
   return launch_route_as<4>(x, wr, T, E, H, topk, renorm, ids, weights, stream);
 }
 
-// 32 tokens at a time, one cooperative launch each.
-template <bool ROUTE>
+// 32 tokens at a time: gate and up, then down.
 nvq_status launch_experts(nvq::moe::ExpertParams p, int64_t T, void* workspace, cudaStream_t stream) {
   using namespace nvq::moe;
-  static std::once_flag once[kMaxDevices];
-  static cudaError_t err[kMaxDevices];
-  const nvq_status st = kernel_opt_in(moe_kernel<ROUTE>, RING_BYTES + kBehindRing, false, once, err, "w4a16_moe: kernel attributes");
+  static std::once_flag once[2][kMaxDevices];
+  static cudaError_t err[2][kMaxDevices];
+  nvq_status st = kernel_opt_in(gate_up_kernel, kGateUpSmem, false, once[0], err[0], "w4a16_moe: kernel attributes");
+  if (st == NVQ_OK)
+    st = kernel_opt_in(down_kernel, RING_BYTES + kBehindRing, false, once[1], err[1], "w4a16_moe: kernel attributes");
   if (st != NVQ_OK) return st;
   const MoeWs W = moe_ws_layout(T, p.H, p.I, p.topk);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.h = reinterpret_cast<__nv_bfloat16*>(ws + W.h);
   p.tickets = reinterpret_cast<uint32_t*>(ws + W.tickets);
   p.partial = reinterpret_cast<float*>(ws + W.partial);
-  p.logits = reinterpret_cast<float*>(ws + W.logits);
-  const int grid = std::min(kMoeMaxGrid, sm_count());
   p.by_topk = FastDiv(p.topk);
-  p.by_grid = FastDiv((uint32_t)grid);
   p.by_g = FastDiv(p.H / 128);
   p.by_rtiles = FastDiv(p.I / 16);
   p.by_gi = FastDiv(p.I / 128);
-  p.etiles = (p.E + 15) / 16;
-  // Slices of K of the router: no more (tile, slice) pairs than CTAs, a 64-wide block of K for each warp.
-  p.slices = std::max(1u, std::min((uint32_t)grid / p.etiles, p.H / 64 / EWARPS));
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
-  cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(ETHREADS, 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   for (int64_t t0 = 0; t0 < T; t0 += kMaxTokens) {
     p.T = (uint32_t)std::min<int64_t>(kMaxTokens, T - t0);
-    p.stage = stage_h(p.T, p.T * p.topk, p.I) ? 1u : 0u;
-    cfg.dynamicSmemBytes = (size_t)layer_smem(p.T, p.T * p.topk, p.I);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_kernel<ROUTE>, p);
-    if (e != cudaSuccess) return cuda_fail(e, "moe_kernel launch");
+    const int64_t pairs = (int64_t)p.T * p.topk, units = std::min<int64_t>(p.E, pairs) * (p.I / 16) * (p.H / 128);
+    // Up to eight units per warp one CTA on each SM, so that the down kernel's CTAs are
+    // resident beside them and have their plan and first weights when h is complete
+    // (448 units: 10.0 us with two, 8.2 with one); more want all warps of an SM
+    // (360448 units: 228 us with two, 414 with one).
+    const int sms = std::min(kMoeMaxGrid / 2, sm_count()), grid = units <= 8 * EWARPS * sms ? sms : 2 * sms;
+    p.by_grid = FastDiv((uint32_t)grid);
+    p.stage = stage_h(p.T, pairs, p.I) ? 1u : 0u;
+    st = launch_dependent("gate_up_kernel", gate_up_kernel, grid, ETHREADS, kGateUpSmem, 0, stream, p);
+    if (st == NVQ_OK)
+      st = launch_dependent("down_kernel", down_kernel, grid, ETHREADS, (size_t)down_smem(p.T, pairs, p.I), 0, stream, p);
+    if (st != NVQ_OK) return st;
     p.x += (size_t)p.T * p.H;
     p.y += (size_t)p.T * p.H;
     if (p.residual) p.residual += (size_t)p.T * p.H;
     p.ids += (size_t)p.T * p.topk;
     p.weights += (size_t)p.T * p.topk;
   }
-  return launch_status("moe_kernel");
+  return NVQ_OK;
 }
 
-nvq::moe::ExpertParams expert_params(const void* x, int32_t* ids, float* weights,
+nvq::moe::ExpertParams expert_params(const void* x, const int32_t* ids, const float* weights,
                                      const void* const (&packed)[4], const void* residual, void* y, int64_t E,
                                      int64_t H, int64_t I, int topk) {
   nvq::moe::ExpertParams p = {};
@@ -971,9 +964,8 @@ nvq_status w4a16_moe_experts(const void* x_bf16, const int32_t* ids, const float
   const nvq_status st = experts_validate("w4a16_moe_experts", x_bf16, ids, weights, packed, residual_bf16, y_bf16, T, E,
                                          H, I, topk, workspace, workspace_bytes);
   if (st != NVQ_OK || T == 0) return st;
-  return launch_experts<false>(expert_params(x_bf16, const_cast<int32_t*>(ids), const_cast<float*>(weights), packed,
-                                             residual_bf16, y_bf16, E, H, I, topk),
-                               T, workspace, static_cast<cudaStream_t>(stream));
+  return launch_experts(expert_params(x_bf16, ids, weights, packed, residual_bf16, y_bf16, E, H, I, topk), T, workspace,
+                        static_cast<cudaStream_t>(stream));
 }
 
 nvq_status w4a16_moe(const void* x_bf16, const void* w_router_bf16, const uint8_t* gate_up_codes,
@@ -988,10 +980,10 @@ nvq_status w4a16_moe(const void* x_bf16, const void* w_router_bf16, const uint8_
   st = experts_validate("w4a16_moe", x_bf16, ids, weights, packed, residual_bf16, y_bf16, T, E, H, I, topk, workspace,
                         workspace_bytes);
   if (st != NVQ_OK || T == 0) return st;
-  nvq::moe::ExpertParams p = expert_params(x_bf16, ids, weights, packed, residual_bf16, y_bf16, E, H, I, topk);
-  p.wr = static_cast<const __nv_bfloat16*>(w_router_bf16);
-  p.renorm = renormalize != 0 ? 1u : 0u;
-  return launch_experts<true>(p, T, workspace, stream);
+  st = launch_route(x_bf16, w_router_bf16, T, E, H, topk, renormalize != 0, ids, weights, stream);
+  if (st != NVQ_OK) return st;
+  return launch_experts(expert_params(x_bf16, ids, weights, packed, residual_bf16, y_bf16, E, H, I, topk), T, workspace,
+                        stream);
 }
 
 // ------------------------------------------------------------------ phase dispatch

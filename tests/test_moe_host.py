@@ -135,7 +135,7 @@ def test_interleave_in_blocks_of_16():
 
 
 # ------------------------------------------------------------------ mirrors of the kernel's index arithmetic
-WARPS, COLS, GRID, UNIT_COST = 16, 8, 148, 28
+WARPS, COLS, GRIDS, UNIT_COST = 8, 8, (148, 296), 28
 
 
 def plan(ids, E):
@@ -226,7 +226,7 @@ def test_gate_up_split_covers_every_unit_once():
     for _ in range(150):
         ids, E = _random_ids(nrng)
         segs, _ = plan(ids, E)
-        rtiles, G, grid = rng.choice([8, 16, 40, 88]), rng.choice([1, 2, 9, 16, 40]), rng.choice([1, 7, GRID])
+        rtiles, G, grid = rng.choice([8, 16, 40, 88]), rng.choice([1, 2, 9, 16, 40]), rng.choice([1, 7, *GRIDS])
         bounds = [first_tile(segs, rtiles, grid, b, ids.size) for b in range(grid + 1)]
         assert bounds == sorted(bounds) and bounds[-1] == len(segs) * rtiles and (not segs or bounds[0] == 0)
         for b in rng.sample(range(grid), min(grid, 6)):
@@ -272,7 +272,7 @@ def test_gate_up_split_covers_every_unit_once():
 def down_cut(U, ntile, grid, b):
     """(half, whole, parts, q, r, F0, F1, n0, n1) of CTA b."""
     total, rounds = U * ntile, -(-U // WARPS)
-    joined = total // WARPS // grid + 3
+    joined = total // WARPS // grid + 5
     half = 2 * ntile <= grid and rounds * 5 <= joined * 8
     whole = half or -(-ntile // grid) * rounds <= joined
     pieces = (2 * ntile if half else ntile) if whole else total
@@ -288,7 +288,7 @@ def test_down_split_covers_every_unit_once_and_finds_every_part():
     rng = random.Random(3)
     modes = set()
     for _ in range(600):
-        grid, ntile, U = rng.choice([2, GRID]), rng.choice([4, 8, 64, 74, 75, 128, 160]), rng.choice([1, 2, 3, 12, 48, 96, 97, 672])
+        grid, ntile, U = rng.choice([2, *GRIDS]), rng.choice([4, 8, 64, 74, 75, 128, 149, 160, 300]), rng.choice([1, 2, 3, 12, 48, 96, 97, 672])
         half, whole_mode, parts, q, r, *_ = down_cut(U, ntile, grid, 0)
         modes.add((half, whole_mode))
         tiles = 2 * ntile if half else ntile
