@@ -8,9 +8,9 @@
 //
 // Three launches chained by programmatic dependent launch: the router, gate and
 // up, down.  (One cooperative launch with grid barriers between the phases was
-// slower for few tokens, 12.3 against 10.0 us for 1344 units of weights, and 5%
-// faster for the largest batches: a grid barrier takes 1.8 us and the gap before a
-// cooperative launch 2.6, a dependent launch 0.75.)  The experts are in the packed
+// slower for few tokens, 12.3 against 9.4 us for 1344 units of weights, and equal
+// for the largest batches, 217 and 219 us for 360448: a grid barrier takes 1.8 us and
+// the gap before a cooperative launch 2.6, a dependent launch 0.75.)  The experts are in the packed
 // form of the decode GEMM (units of 32 rows x 128 k), gate and up rows in turn by
 // 16, so that one unit holds 16 gate rows (MMA tile 0) and the matching 16 up rows
 // (tile 1) and a lane has both halves of its h.  Weights are read from memory once
@@ -300,8 +300,8 @@ route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restric
 }
 
 // ------------------------------------------------------------------ segments
-constexpr int EWARPS = 8;
-constexpr int ETHREADS = EWARPS * 32;
+// The expert kernels are built for W = 8 warps per CTA (few tokens: a CTA of each on
+// an SM) and W = 16 (one CTA per SM with all its warps).
 constexpr uint32_t COLS = 8;        // tokens of one segment
 
 // n / d for n < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d), 2^l >= d,
@@ -346,7 +346,7 @@ struct Plan {
   uint16_t seg_e[kMaxPairs], seg_s[kMaxPairs];   // segment -> expert, first slot
   uint8_t seg_n[kMaxPairs];         // its tokens, 1 .. COLS
   uint8_t token[kMaxPairs];         // slot -> token
-  uint32_t warp_sum[EWARPS];
+  uint32_t warp_sum[16];
   uint32_t segments;
 };
 
@@ -361,12 +361,14 @@ struct DownCut {
 // of one expert.  An id outside [0, E) is no choice; an expert that a token names
 // twice counts once, with the sum of the weights (the same sum of products), so
 // that a segment never holds a token twice.  Called by the whole CTA.
+template <int W>
 __device__ __forceinline__ void build_plan(Plan& pl, const ExpertParams& p) {
+  constexpr uint32_t THREADS = W * 32, PER = kMaxPairs / THREADS;      // pairs, and experts, per thread
   const uint32_t P = p.T * p.topk, tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
   if (P <= 32) {                    // one warp, a pair per lane; experts in the order of their first pair
     if (warp == 0) {
-      const int32_t id = lane < P ? p.ids[lane] : -1;
-      const float w = lane < P ? p.weights[lane] : 0.f;
+      const int32_t id = lane < P ? __ldcg(p.ids + lane) : -1;
+      const float w = lane < P ? __ldcg(p.weights + lane) : 0.f;
       const uint32_t t = p.by_topk.div(lane);
       const bool valid = lane < P && (uint32_t)id < p.E;
       const uint32_t lt = (1u << lane) - 1u;
@@ -410,18 +412,17 @@ __device__ __forceinline__ void build_plan(Plan& pl, const ExpertParams& p) {
     __syncthreads();
     return;
   }
-  for (uint32_t i = tid; i < P; i += ETHREADS) {
-    pl.id[i] = p.ids[i];
-    pl.w[i] = p.weights[i];
+  for (uint32_t i = tid; i < P; i += THREADS) {
+    pl.id[i] = __ldcg(p.ids + i);
+    pl.w[i] = __ldcg(p.weights + i);
   }
-  static_assert(kMaxExperts == 2 * ETHREADS && kMaxPairs == 2 * ETHREADS, "two experts and two pairs per thread");
-  pl.mask[tid] = 0u;
-  pl.mask[tid + ETHREADS] = 0u;
+  static_assert(kMaxExperts == kMaxPairs && kMaxPairs % THREADS == 0, "the same number of each per thread");
+  for (uint32_t k = 0; k < PER; ++k) pl.mask[tid + k * THREADS] = 0u;
   __syncthreads();
-  bool first[2];
+  bool first[PER];
 #pragma unroll
-  for (uint32_t k = 0; k < 2; ++k) {
-    const uint32_t i = tid + k * ETHREADS, t = p.by_topk.div(i), j0 = t * p.topk;
+  for (uint32_t k = 0; k < PER; ++k) {
+    const uint32_t i = tid + k * THREADS, t = p.by_topk.div(i), j0 = t * p.topk;
     const int32_t id = i < P ? pl.id[i] : -1;
     first[k] = (uint32_t)id < p.E;
     if (first[k]) {
@@ -436,8 +437,13 @@ __device__ __forceinline__ void build_plan(Plan& pl, const ExpertParams& p) {
     }
   }
   __syncthreads();
-  const uint32_t n0 = __popc(pl.mask[2 * tid]), n1 = __popc(pl.mask[2 * tid + 1]);
-  const uint32_t add = (n0 + n1) | ((n0 + COLS - 1) / COLS + (n1 + COLS - 1) / COLS) << 16;
+  // PER experts per thread: slots in the low half, segments in the high half of one sum.
+  uint32_t n[PER], add = 0;
+#pragma unroll
+  for (uint32_t k = 0; k < PER; ++k) {
+    n[k] = __popc(pl.mask[PER * tid + k]);
+    add += n[k] | ((n[k] + COLS - 1) / COLS) << 16;
+  }
   uint32_t inc = add;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -450,22 +456,22 @@ __device__ __forceinline__ void build_plan(Plan& pl, const ExpertParams& p) {
   for (uint32_t w = 0; w < warp; ++w) before += pl.warp_sum[w];
   uint32_t slot = before & 0xFFFFu, seg = before >> 16;
 #pragma unroll
-  for (uint32_t k = 0; k < 2; ++k) {
-    const uint32_t n = k ? n1 : n0;
-    pl.first[2 * tid + k] = (uint16_t)slot;
-    for (uint32_t q = 0; q < n; q += COLS, ++seg) {
-      pl.seg_e[seg] = (uint16_t)(2 * tid + k);
+  for (uint32_t k = 0; k < PER; ++k) {
+    const uint32_t e = PER * tid + k;
+    pl.first[e] = (uint16_t)slot;
+    for (uint32_t q = 0; q < n[k]; q += COLS, ++seg) {
+      pl.seg_e[seg] = (uint16_t)e;
       pl.seg_s[seg] = (uint16_t)(slot + q);
-      pl.seg_n[seg] = (uint8_t)min(COLS, n - q);
+      pl.seg_n[seg] = (uint8_t)min(COLS, n[k] - q);
     }
-    slot += n;
+    slot += n[k];
   }
-  if (tid == ETHREADS - 1) pl.segments = seg;
+  if (tid == THREADS - 1) pl.segments = seg;
   __syncthreads();
 #pragma unroll
-  for (uint32_t k = 0; k < 2; ++k)
+  for (uint32_t k = 0; k < PER; ++k)
     if (first[k]) {
-      const uint32_t i = tid + k * ETHREADS, t = p.by_topk.div(i);
+      const uint32_t i = tid + k * THREADS, t = p.by_topk.div(i);
       const uint32_t at = pl.first[pl.id[i]] + __popc(pl.mask[pl.id[i]] & ((1u << t) - 1u));
       pl.pair[at] = (uint16_t)i;
       pl.token[at] = (uint8_t)t;
@@ -636,36 +642,41 @@ __device__ __forceinline__ uint32_t ticket(uint32_t* counter) {
 
 // ------------------------------------------------------------------ the layer
 constexpr int RING = 3;
-constexpr int RING_BYTES = EWARPS * RING * SLOT;
 // Shared memory behind the ring.  Gate and up: the cut tiles (two of 16 x 8 x 2 sums
 // per warp) and the column offsets of up to kOffsets (segment, group) pairs.  Down: the
-// per-token rows of each warp and, where it fits within kBehindRing with them, all of h
-// (P pairs of I values, two halves each): a few tokens' h, which every CTA reads whole.
-// Both kernels fit on an SM twice, or once each.
+// per-token rows of each warp and, where it fits with them, all of h (P pairs of I
+// values, two halves each): a few tokens' h, which every CTA reads whole.
 constexpr uint32_t kOffsets = 512;
-constexpr int kCutTiles = EWARPS * 2 * 1024;
-constexpr int kGateUpSmem = RING_BYTES + kCutTiles + (int)kOffsets * 32;
-constexpr int kBehindRing = 40 * 1024;
-constexpr bool stage_h(int64_t T, int64_t P, int64_t I) { return EWARPS * T * 32 * 4 + P * I * 4 <= kBehindRing; }
-constexpr int down_smem(int64_t T, int64_t P, int64_t I) {
-  return RING_BYTES + (int)(EWARPS * T * 32 * 4 + (stage_h(T, P, I) ? P * I * 4 : 0));
-}
-static_assert(EWARPS * kMaxTokens * 32 * 4 <= kBehindRing, "the rows of the most tokens");
-static_assert(2 * (kGateUpSmem + sizeof(Plan) + 1024) <= 228 * 1024 && 2 * (RING_BYTES + kBehindRing + sizeof(Plan) + 1024) <= 228 * 1024,
-              "two CTAs per SM");
+template <int W>
+struct Smem {
+  static constexpr int RING_BYTES = W * RING * SLOT;
+  static constexpr int CUT_TILES = W * 2 * 1024;
+  static constexpr int GATE_UP = RING_BYTES + CUT_TILES + (int)kOffsets * 32;
+  static constexpr int BEHIND_RING = W == 8 ? 40 * 1024 : 64 * 1024;
+  static constexpr bool stage_h(int64_t T, int64_t P, int64_t I) { return W * T * 32 * 4 + P * I * 4 <= BEHIND_RING; }
+  static constexpr int down(int64_t T, int64_t P, int64_t I) {
+    return RING_BYTES + (int)(W * T * 32 * 4 + (stage_h(T, P, I) ? P * I * 4 : 0));
+  }
+  static constexpr int PER_CTA = (GATE_UP > RING_BYTES + BEHIND_RING ? GATE_UP : RING_BYTES + BEHIND_RING) + (int)sizeof(Plan) + 1024;
+  static_assert(W * kMaxTokens * 32 * 4 <= BEHIND_RING, "the rows of the most tokens");
+  static_assert((W == 8 ? 2 : 1) * PER_CTA <= 228 * 1024, "what is to be on an SM at once");
+};
 
-// Down: a round (one unit per warp) takes about 0.6 us, 0.4 us for one row tile of the
-// unit; joining cut tiles through memory takes about 2.5 us, four rounds.  So: half tiles (16 columns)
-// where that leaves no more of them than CTAs and is not slower, whole tiles, or even
-// parts of the flat sequence of units.
+// Down: half tiles (16 columns) where that leaves no more of them than CTAs and is not
+// slower, whole tiles, or even parts of the flat sequence of units.  With 8 warps a
+// round (one unit per warp) takes about 0.6 us, 0.4 us for one row tile of the unit, and
+// joining cut tiles through memory 2.5 us, which with the rounding down of `joined` is
+// five rounds.  With 16 warps a round takes longer, so four: 21.9 us for 16 experts of
+// 704 units (24.6 with two), 45.0 for 52 of 704 (47.1 with six).
+template <int W>
 __device__ __forceinline__ DownCut cut_down(const ExpertParams& p, uint32_t segments, uint32_t ntile, uint32_t Gi) {
   DownCut d;
   const uint32_t U = segments * Gi, total = U * ntile, grid = gridDim.x;
-  const uint32_t rounds = (U + EWARPS - 1) / EWARPS, joined = p.by_grid.div(total / EWARPS) + 5;
+  const uint32_t rounds = (U + W - 1) / W, joined = p.by_grid.div(total / W) + (W == 8 ? 5 : 4);
   d.half = 2 * ntile <= grid && rounds * 5 <= joined * 8;
   d.whole = d.half || p.by_grid.div(ntile + grid - 1) * rounds <= joined;
   const uint32_t pieces = d.whole ? (d.half ? 2 * ntile : ntile) : total;
-  d.parts = min(grid, d.whole ? pieces : (total + EWARPS - 1) / EWARPS);
+  d.parts = min(grid, d.whole ? pieces : (total + W - 1) / W);
   d.q = d.parts == grid ? p.by_grid.div(pieces) : pieces / max(d.parts, 1u);
   d.r = pieces - d.q * d.parts;
   const uint32_t b = blockIdx.x, P0 = b * d.q + min(b, d.r), P1 = P0 + d.q + (b < d.r ? 1u : 0u);
@@ -684,24 +695,27 @@ __device__ __forceinline__ DownCut cut_down(const ExpertParams& p, uint32_t segm
 // and 16 up rows), H / 128 units.  A CTA owns whole tiles (segment-major, so that
 // it stays with one expert's rows of x), its warps equal runs of their units; a
 // tile inside one run is finished in registers, the others through shared memory.
-__global__ void __launch_bounds__(ETHREADS, 2) gate_up_kernel(const ExpertParams p) {
+template <int W>
+__global__ void __launch_bounds__(W * 32, 16 / W) gate_up_kernel(const ExpertParams p) {
+  using S = Smem<W>;
+  constexpr uint32_t THREADS = W * 32;
   extern __shared__ __align__(16) uint8_t esm[];
   __shared__ Plan pl;
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, g8 = lane >> 2, c = lane & 3u;
   const uint32_t H = p.H, I = p.I, P = p.T * p.topk;
   grid_dependency_wait();
   grid_launch_dependents();
-  build_plan(pl, p);
+  build_plan<W>(pl, p);
   const uint32_t segments = pl.segments, G = H / 128, rtiles = I / 16;
   const size_t low = (size_t)P * I;                                    // from a high half of h to its low half
-  for (uint32_t i = blockIdx.x * ETHREADS + threadIdx.x; i < H / 32; i += gridDim.x * ETHREADS) p.tickets[i] = 0u;
+  for (uint32_t i = blockIdx.x * THREADS + threadIdx.x; i < H / 32; i += gridDim.x * THREADS) p.tickets[i] = 0u;
   Ring<RING> ring;
   ring.init(esm, warp, lane);
   {
-    float* part = reinterpret_cast<float*>(esm + RING_BYTES);          // [EWARPS][2][256]
+    float* part = reinterpret_cast<float*>(esm + S::RING_BYTES);          // [W][2][256]
     // A unit of a segment with n tokens costs about kUnitCost + n: its n rows of x are
-    // read next to the weights (8192 tokens' worth of measurement: 111 us a CTA for
-    // n = 1, 122 for 4, 134 for 7).  The segments' costs are cut into equal parts; with
+    // read next to the weights (T 32, H 4096, I 1408, cut evenly: a CTA took 111 us where
+    // n was 1 throughout, 122 for 4, 134 for 7).  The segments' costs are cut into equal parts; with
     // as many slots before a segment as tokens, the cost before it is a sum of two
     // known numbers.
     constexpr uint32_t kUnitCost = 28;
@@ -729,7 +743,7 @@ __global__ void __launch_bounds__(ETHREADS, 2) gate_up_kernel(const ExpertParams
       else mine = t - T0;
     }
     const uint32_t L = mine * G;                                       // this CTA's units
-    auto cut = [&](uint32_t w) { return (uint32_t)((uint64_t)L * w / EWARPS); };
+    auto cut = [&](uint32_t w) { return (uint32_t)((uint64_t)L * w / W); };
     const uint32_t f0 = cut(warp), f1 = cut(warp + 1);
 
     // h of one finished tile from this lane's sums: rows (h columns) g8 and g8 + 8, tokens 2 c and 2 c + 1.
@@ -788,9 +802,10 @@ __global__ void __launch_bounds__(ETHREADS, 2) gate_up_kernel(const ExpertParams
     // segments, which each of their row tiles needs again.
     const uint32_t seg0 = p.by_rtiles.div(T0), nseg = mine ? p.by_rtiles.div(T0 + mine - 1) - seg0 + 1 : 0u;
     const bool given = nseg * G <= kOffsets;
-    float2* offsets = reinterpret_cast<float2*>(esm + RING_BYTES + kCutTiles);   // [segment][group][c]
+    float2* offsets = reinterpret_cast<float2*>(esm + S::RING_BYTES + S::CUT_TILES);   // [segment][group][c]
     if (given) {
-      for (uint32_t i = warp; i < nseg * G; i += EWARPS) {
+#pragma unroll 2
+      for (uint32_t i = warp; i < nseg * G; i += W) {
         const uint32_t s = p.by_g.div(i);
         uint4 b[4];
         float off[2];
@@ -852,7 +867,7 @@ __global__ void __launch_bounds__(ETHREADS, 2) gate_up_kernel(const ExpertParams
     const uint32_t tb = p.by_g.div(f0) * G, te = tb + G;
     if (f0 != tb && f0 < L && cut(warp - 1) <= tb) {
       float acc[2][4] = {};
-      for (uint32_t w = warp - 1; w < EWARPS && cut(w) < te; ++w) {
+      for (uint32_t w = warp - 1; w < W && cut(w) < te; ++w) {
         if (cut(w) == cut(w + 1)) continue;
         const float4* q = reinterpret_cast<const float4*>(part + (w * 2 + (cut(w) >= tb ? 0 : 1)) * 256) + lane;
         const float4 v0 = q[0], v1 = q[32];
@@ -871,7 +886,10 @@ __global__ void __launch_bounds__(ETHREADS, 2) gate_up_kernel(const ExpertParams
 // shared-memory rows, the warps' rows are added in order.  A tile that several parts
 // share is finished by the CTA that comes last (a ticket per tile), which adds the
 // parts' sums in order: nothing waits, and the result does not depend on who came last.
-__global__ void __launch_bounds__(ETHREADS, 2) down_kernel(const ExpertParams p) {
+template <int W>
+__global__ void __launch_bounds__(W * 32, 16 / W) down_kernel(const ExpertParams p) {
+  using S = Smem<W>;
+  constexpr uint32_t THREADS = W * 32;
   extern __shared__ __align__(16) uint8_t esm[];
   __shared__ Plan pl;
   __shared__ uint32_t last[2];
@@ -881,15 +899,15 @@ __global__ void __launch_bounds__(ETHREADS, 2) down_kernel(const ExpertParams p)
   // This kernel is launched when every CTA of the gate and up kernel is past its own
   // wait, so ids and weights are final: the plan, the cut and the first weights do not
   // wait for h.
-  build_plan(pl, p);
+  build_plan<W>(pl, p);
   const uint32_t segments = pl.segments;
   const size_t low = (size_t)P * I;                                    // from a high half of h to its low half
-  const DownCut cd = cut_down(p, segments, ntile, Gi);
+  const DownCut cd = cut_down<W>(p, segments, ntile, Gi);
   Ring<RING> ring;
   const uint32_t U = segments * Gi;
   if (segments == 0) {                                                 // no token has an expert
     grid_dependency_wait();
-    for (size_t i = (size_t)blockIdx.x * ETHREADS + threadIdx.x; i < (size_t)T * H; i += (size_t)gridDim.x * ETHREADS)
+    for (size_t i = (size_t)blockIdx.x * THREADS + threadIdx.x; i < (size_t)T * H; i += (size_t)gridDim.x * THREADS)
       p.y[i] = p.residual ? p.residual[i] : __float2bfloat16_rn(0.f);
     return;
   }
@@ -899,8 +917,8 @@ __global__ void __launch_bounds__(ETHREADS, 2) down_kernel(const ExpertParams p)
   // This warp's share [lo, hi) of the units of tile n that belong to this CTA.
   auto share = [&](uint32_t n, uint32_t& lo, uint32_t& hi) {
     const uint32_t tb = n * U, from = max(F0, tb) - tb, len = min(F1, tb + U) - tb - from;
-    lo = from + (uint32_t)((uint64_t)len * warp / EWARPS);
-    hi = from + (uint32_t)((uint64_t)len * (warp + 1) / EWARPS);
+    lo = from + (uint32_t)((uint64_t)len * warp / W);
+    hi = from + (uint32_t)((uint64_t)len * (warp + 1) / W);
   };
   uint32_t rn = n0, rseg = 0, rleft = 0, rem = 0, lo = 0, hi = 0;      // the units being requested
   auto request_from = [&](uint32_t a, uint32_t b) {
@@ -933,8 +951,8 @@ __global__ void __launch_bounds__(ETHREADS, 2) down_kernel(const ExpertParams p)
 #pragma unroll 1
     for (int i = 0; i < RING; ++i) fill();
   }
-  constexpr int OUTS = kMaxTokens * 32 / ETHREADS;                     // outputs of a tile per thread
-  float* sums = reinterpret_cast<float*>(esm + RING_BYTES);            // [EWARPS][T][width]
+  constexpr int OUTS = kMaxTokens * 32 / THREADS;                     // outputs of a tile per thread
+  float* sums = reinterpret_cast<float*>(esm + S::RING_BYTES);            // [W][T][width]
   float* rows = sums + warp * outs;
   const uint32_t wlog = half ? 4 : 5;
   auto output_at = [&](uint32_t n, uint32_t i) { return (size_t)(i >> wlog) * H + n * width + (i & (width - 1)); };
@@ -943,7 +961,7 @@ __global__ void __launch_bounds__(ETHREADS, 2) down_kernel(const ExpertParams p)
     if (p.residual)
 #pragma unroll
       for (int k = 0; k < OUTS; ++k) {
-        const uint32_t i = threadIdx.x + k * ETHREADS;
+        const uint32_t i = threadIdx.x + k * THREADS;
         if (i < outs) r[k] = reinterpret_cast<const uint16_t*>(p.residual)[output_at(n, i)];
       }
   };
@@ -962,9 +980,9 @@ __global__ void __launch_bounds__(ETHREADS, 2) down_kernel(const ExpertParams p)
 
   const __nv_bfloat16* h = p.h;
   if (p.stage) {                                                       // all of h fits behind the rows
-    float* to = sums + EWARPS * outs;
+    float* to = sums + W * outs;
     if (works)
-      for (uint32_t i = threadIdx.x * 16; i < low * 4; i += ETHREADS * 16)
+      for (uint32_t i = threadIdx.x * 16; i < low * 4; i += THREADS * 16)
         cp_async16(smem_addr(to) + i, reinterpret_cast<const uint8_t*>(p.h) + i);
     cp_commit();
     cp_wait<0>();
@@ -1078,20 +1096,20 @@ __global__ void __launch_bounds__(ETHREADS, 2) down_kernel(const ExpertParams p)
     auto warps_sum = [&](uint32_t i) {
       float s = 0.f;
 #pragma unroll
-      for (uint32_t w = 0; w < EWARPS; ++w) s += sums[w * outs + i];
+      for (uint32_t w = 0; w < W; ++w) s += sums[w * outs + i];
       return s;
     };
     if (whole) {
 #pragma unroll
       for (int k = 0; k < OUTS; ++k) {
-        const uint32_t i = threadIdx.x + k * ETHREADS;
+        const uint32_t i = threadIdx.x + k * THREADS;
         if (i < outs) store(n, i, warps_sum(i), res[k]);
       }
       __syncthreads();                                                 // the rows are cleared for the next tile
     } else {
       // Part b's slot for this tile: 0 if the tile is the first of its range, else 1.
       float* to = p.partial + ((size_t)2 * blockIdx.x + (F0 >= tb ? 0 : 1)) * outs;
-      for (uint32_t i = threadIdx.x; i < outs; i += ETHREADS) __stcg(to + i, warps_sum(i));
+      for (uint32_t i = threadIdx.x; i < outs; i += THREADS) __stcg(to + i, warps_sum(i));
       __syncthreads();
       if (threadIdx.x == 0) last[n == n0 ? 0 : 1] = ticket(p.tickets + n) == owner(tb + U - 1) - owner(tb) ? 1u : 0u;
     }
@@ -1107,7 +1125,7 @@ __global__ void __launch_bounds__(ETHREADS, 2) down_kernel(const ExpertParams p)
     residual_of(n, res);
 #pragma unroll
     for (int j = 0; j < OUTS; ++j) {
-      const uint32_t i = threadIdx.x + j * ETHREADS;
+      const uint32_t i = threadIdx.x + j * THREADS;
       if (i < outs) {
         float s = __ldcg(from + i);
 #pragma unroll 4

@@ -788,9 +788,9 @@ nvq_status w4a16_sparse24_gemm(const void* x_bf16, const uint8_t* packed, const 
 // ------------------------------------------------------------------ mixture of experts
 namespace {
 
-// CTAs of the expert kernels: two on each of a B200's SMs.  A constant, so that the
+// CTAs of an expert kernel: one on each of a B200's SMs.  A constant, so that the
 // workspace (two partial tiles per CTA) can be sized without a device.
-constexpr int kMoeMaxGrid = 2 * 148;
+constexpr int kMoeMaxGrid = 148;
 // H and I, and one expert's down matrix: units of 512 segments are counted in 31 bits.
 constexpr int64_t kMoeMaxDim = (int64_t)1 << 20, kMoeMaxWeight = (int64_t)1 << 33;
 
@@ -878,37 +878,47 @@ nvq_status launch_route(const void* x, const void* wr, int64_t T, int64_t E, int
   return launch_route_as<4>(x, wr, T, E, H, topk, renorm, ids, weights, stream);
 }
 
-// 32 tokens at a time: gate and up, then down.
-nvq_status launch_experts(nvq::moe::ExpertParams p, int64_t T, void* workspace, cudaStream_t stream) {
+// Gate and up, then down, for p.T <= 32 tokens; W: warps per CTA.
+template <int W>
+nvq_status launch_experts_32(nvq::moe::ExpertParams p, int grid, cudaStream_t stream) {
   using namespace nvq::moe;
+  using S = Smem<W>;
   static std::once_flag once[2][kMaxDevices];
   static cudaError_t err[2][kMaxDevices];
-  nvq_status st = kernel_opt_in(gate_up_kernel, kGateUpSmem, false, once[0], err[0], "w4a16_moe: kernel attributes");
+  nvq_status st = kernel_opt_in(gate_up_kernel<W>, S::GATE_UP, false, once[0], err[0], "w4a16_moe: kernel attributes");
   if (st == NVQ_OK)
-    st = kernel_opt_in(down_kernel, RING_BYTES + kBehindRing, false, once[1], err[1], "w4a16_moe: kernel attributes");
+    st = kernel_opt_in(down_kernel<W>, S::RING_BYTES + S::BEHIND_RING, false, once[1], err[1], "w4a16_moe: kernel attributes");
   if (st != NVQ_OK) return st;
+  const int64_t pairs = (int64_t)p.T * p.topk;
+  p.stage = S::stage_h(p.T, pairs, p.I) ? 1u : 0u;
+  st = launch_dependent("gate_up_kernel", gate_up_kernel<W>, grid, W * 32, (size_t)S::GATE_UP, 0, stream, p);
+  if (st == NVQ_OK)
+    st = launch_dependent("down_kernel", down_kernel<W>, grid, W * 32, (size_t)S::down(p.T, pairs, p.I), 0, stream, p);
+  return st;
+}
+
+// 32 tokens at a time.
+nvq_status launch_experts(nvq::moe::ExpertParams p, int64_t T, void* workspace, cudaStream_t stream) {
+  using namespace nvq::moe;
   const MoeWs W = moe_ws_layout(T, p.H, p.I, p.topk);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.h = reinterpret_cast<__nv_bfloat16*>(ws + W.h);
   p.tickets = reinterpret_cast<uint32_t*>(ws + W.tickets);
   p.partial = reinterpret_cast<float*>(ws + W.partial);
+  const int grid = std::min(kMoeMaxGrid, sm_count());
   p.by_topk = FastDiv(p.topk);
+  p.by_grid = FastDiv((uint32_t)grid);
   p.by_g = FastDiv(p.H / 128);
   p.by_rtiles = FastDiv(p.I / 16);
   p.by_gi = FastDiv(p.I / 128);
   for (int64_t t0 = 0; t0 < T; t0 += kMaxTokens) {
     p.T = (uint32_t)std::min<int64_t>(kMaxTokens, T - t0);
-    const int64_t pairs = (int64_t)p.T * p.topk, units = std::min<int64_t>(p.E, pairs) * (p.I / 16) * (p.H / 128);
-    // Up to eight units per warp one CTA on each SM, so that the down kernel's CTAs are
-    // resident beside them and have their plan and first weights when h is complete
-    // (448 units: 10.0 us with two, 8.2 with one); more want all warps of an SM
-    // (360448 units: 228 us with two, 414 with one).
-    const int sms = std::min(kMoeMaxGrid / 2, sm_count()), grid = units <= 8 * EWARPS * sms ? sms : 2 * sms;
-    p.by_grid = FastDiv((uint32_t)grid);
-    p.stage = stage_h(p.T, pairs, p.I) ? 1u : 0u;
-    st = launch_dependent("gate_up_kernel", gate_up_kernel, grid, ETHREADS, kGateUpSmem, 0, stream, p);
-    if (st == NVQ_OK)
-      st = launch_dependent("down_kernel", down_kernel, grid, ETHREADS, (size_t)down_smem(p.T, pairs, p.I), 0, stream, p);
+    const int64_t units = std::min<int64_t>(p.E, (int64_t)p.T * p.topk) * (p.I / 16) * (p.H / 128);
+    // Up to two units of gate and up weights per warp of eight-warp CTAs: both kernels'
+    // CTAs fit on an SM, and down has its plan and first weights when h is complete
+    // (512 units: 8.2 us, and 8.9 with 16 warps; 2048: 10.5 and 10.8).  More want all
+    // warps on the weights (4096 units: 13.5 us with 8 warps, 12.2 with 16; 73216: 53 and 45).
+    const nvq_status st = units <= 2 * 8 * grid ? launch_experts_32<8>(p, grid, stream) : launch_experts_32<16>(p, grid, stream);
     if (st != NVQ_OK) return st;
     p.x += (size_t)p.T * p.H;
     p.y += (size_t)p.T * p.H;

@@ -135,7 +135,7 @@ def test_interleave_in_blocks_of_16():
 
 
 # ------------------------------------------------------------------ mirrors of the kernel's index arithmetic
-WARPS, COLS, GRIDS, UNIT_COST = 8, 8, (148, 296), 28
+WARPS, COLS, GRIDS, UNIT_COST = (8, 16), 8, (148, 132), 28
 
 
 def plan(ids, E):
@@ -226,6 +226,7 @@ def test_gate_up_split_covers_every_unit_once():
     for _ in range(150):
         ids, E = _random_ids(nrng)
         segs, _ = plan(ids, E)
+        warps = rng.choice(WARPS)
         rtiles, G, grid = rng.choice([8, 16, 40, 88]), rng.choice([1, 2, 9, 16, 40]), rng.choice([1, 7, *GRIDS])
         bounds = [first_tile(segs, rtiles, grid, b, ids.size) for b in range(grid + 1)]
         assert bounds == sorted(bounds) and bounds[-1] == len(segs) * rtiles and (not segs or bounds[0] == 0)
@@ -233,8 +234,8 @@ def test_gate_up_split_covers_every_unit_once():
             mine = bounds[b + 1] - bounds[b]
             length = mine * G
             direct, slots = set(), {}
-            for w in range(WARPS):
-                f0, f1 = cut(length, w, WARPS), cut(length, w + 1, WARPS)
+            for w in range(warps):
+                f0, f1 = cut(length, w, warps), cut(length, w + 1, warps)
                 if f0 == f1:
                     continue
                 tile, g, start = f0 // G, f0 % G, f0
@@ -251,15 +252,15 @@ def test_gate_up_split_covers_every_unit_once():
                 if g:
                     slots[w, 0 if f0 // G == (f1 - 1) // G else 1] = (tile, start, f1)
             finished = set()
-            for w in range(1, WARPS):
-                f0 = cut(length, w, WARPS)
+            for w in range(1, warps):
+                f0 = cut(length, w, warps)
                 tb = f0 // G * G
                 te = tb + G
-                if f0 != tb and f0 < length and cut(length, w - 1, WARPS) <= tb:
+                if f0 != tb and f0 < length and cut(length, w - 1, warps) <= tb:
                     at, k = tb, w - 1
-                    while k < WARPS and cut(length, k, WARPS) < te:
-                        a = cut(length, k, WARPS)
-                        if a != cut(length, k + 1, WARPS):
+                    while k < warps and cut(length, k, warps) < te:
+                        a = cut(length, k, warps)
+                        if a != cut(length, k + 1, warps):
                             tile, s0, s1 = slots.pop((k, 0 if a >= tb else 1))
                             assert tile == tb // G and s0 == at
                             at = s1
@@ -269,14 +270,14 @@ def test_gate_up_split_covers_every_unit_once():
             assert not slots and finished | direct == set(range(mine)) and not finished & direct
 
 
-def down_cut(U, ntile, grid, b):
-    """(half, whole, parts, q, r, F0, F1, n0, n1) of CTA b."""
-    total, rounds = U * ntile, -(-U // WARPS)
-    joined = total // WARPS // grid + 5
+def down_cut(U, ntile, grid, b, warps):
+    """(half, whole, parts, q, r, F0, F1, n0, n1) of CTA b, of so many warps."""
+    total, rounds = U * ntile, -(-U // warps)
+    joined = total // warps // grid + (5 if warps == 8 else 4)
     half = 2 * ntile <= grid and rounds * 5 <= joined * 8
     whole = half or -(-ntile // grid) * rounds <= joined
     pieces = (2 * ntile if half else ntile) if whole else total
-    parts = min(grid, pieces if whole else -(-total // WARPS))
+    parts = min(grid, pieces if whole else -(-total // warps))
     q, r = pieces // parts, pieces % parts
     P0, P1 = b * q + min(b, r), (b + 1) * q + min(b + 1, r)
     k = U if whole else 1
@@ -288,15 +289,16 @@ def test_down_split_covers_every_unit_once_and_finds_every_part():
     rng = random.Random(3)
     modes = set()
     for _ in range(600):
+        warps = rng.choice(WARPS)
         grid, ntile, U = rng.choice([2, *GRIDS]), rng.choice([4, 8, 64, 74, 75, 128, 149, 160, 300]), rng.choice([1, 2, 3, 12, 48, 96, 97, 672])
-        half, whole_mode, parts, q, r, *_ = down_cut(U, ntile, grid, 0)
+        half, whole_mode, parts, q, r, *_ = down_cut(U, ntile, grid, 0, warps)
         modes.add((half, whole_mode))
         tiles = 2 * ntile if half else ntile
         owner = lambda u: u // (q + 1) if u < r * (q + 1) else r + (u - r * (q + 1)) // q   # noqa: E731
         bound = lambda b: (b * q + min(b, r))                                            # noqa: E731
         count, slot_of, whole, end = {}, {}, set(), 0
         for b in range(grid):
-            *_, F0, F1, n0, n1 = down_cut(U, ntile, grid, b)
+            *_, F0, F1, n0, n1 = down_cut(U, ntile, grid, b, warps)
             if n0 > n1:
                 assert b >= parts
                 continue
@@ -316,9 +318,9 @@ def test_down_split_covers_every_unit_once_and_finds_every_part():
                 lo = max(F0, tb) - tb
                 size = min(F1, tb + U) - tb - lo
                 at = lo
-                for w in range(WARPS):                        # the warps' shares follow one another
-                    assert lo + size * w // WARPS == at
-                    at = lo + size * (w + 1) // WARPS
+                for w in range(warps):                        # the warps' shares follow one another
+                    assert lo + size * w // warps == at
+                    at = lo + size * (w + 1) // warps
                 assert at == lo + size
             assert set(cut_tiles) <= {n0, n1} and not (whole_mode and cut_tiles)
         assert end == tiles * U
