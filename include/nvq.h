@@ -349,8 +349,10 @@ nvq_status w4a16_gemm(const void* x_bf16, const uint8_t* packed_codes, const voi
 
 /* w4a16_gemm with an epilogue: arguments, shape rules and launch behaviour as
  * there (bias and residual are read after the wait on the preceding kernel; an
- * in-place residual is read once, also in calls of several passes).  x may not
- * overlap y. */
+ * in-place residual is read once, also in calls of several passes).  For M <= 8
+ * the sums are w4a16_gemm's bit for bit; larger M goes through the tcgen05 tensor
+ * cores with exact products, FP32 sums and scales in FP32 in an order of its own,
+ * fixed by the shapes, and is as fast up to M = 32.  x may not overlap y. */
 nvq_status w4a16_gemm_epilogue(const void* x_bf16, const uint8_t* packed_codes, const void* packed_scales,
                                void* y_bf16, int64_t M, int64_t N, int64_t K, const nvq_epilogue* epilogue,
                                void* stream);

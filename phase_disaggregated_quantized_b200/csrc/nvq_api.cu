@@ -18,6 +18,7 @@
 #include "nvfp4_quantize.cuh"
 #include "ptx.cuh"
 #include "w4a16_gemm.cuh"
+#include "w4a16_tmem.cuh"
 
 namespace nvq {
 // Diagnostic kernel: lane 0 initialises an mbarrier for one arrival that never
@@ -185,6 +186,44 @@ nvq_status launch_dependent(const char* where, void (*kernel)(P...), int grid, i
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e != cudaSuccess) return cuda_fail(e, where);
   return launch_status(where);
+}
+
+// More than 8 rows with an epilogue: how many CTAs of a cluster share a 128-row tile's
+// k-groups.  As many as make the longest CTA's work least: rounds over the clusters that a
+// B200 holds at once with one CTA per SM (148 CTAs, 74 clusters of 2, 33 of 4, 15 of 8),
+// each of a slice of the groups (0.3 to 0.4 us per group) and the end of a tile (kEnd, in
+// half groups: fitted to M 16 and 32, N and K from 64 to 24576).  32 rows, one to eight
+// CTAs: N K 64 8192: 26.5, 15.7, 10.7, 7.9 us; 1024 1024: 6.7, 6.4, 6.5, 7.8; 4096 4096:
+// 16.5, 11.6, 9.5, 20.0; 24576 4096: 33.1, 34.1, 47.0, 84.6.
+struct TmemSplit {
+  uint32_t slog;
+  uint64_t rounds, clusters;
+};
+TmemSplit w4a16_tmem_split(int64_t M, int64_t N, int64_t K, int64_t rows) {
+  constexpr uint64_t kAtOnce[4] = {148, 74, 33, 15}, kEnd[4] = {6, 15, 18, 24};
+  const uint64_t tiles = (uint64_t)((N + 127) / 128) * (uint64_t)((M + rows - 1) / rows), G = (uint64_t)K / 128;
+  TmemSplit best = {};
+  uint64_t least = ~0ull;
+  for (uint32_t l = 0; l < 4 && (1ull << l) <= G; ++l) {
+    const uint64_t rounds = (tiles + kAtOnce[l] - 1) / kAtOnce[l], cost = rounds * (2 * ((G + (1ull << l) - 1) >> l) + kEnd[l]);
+    if (cost < least) {
+      least = cost;
+      best = {l, rounds, (tiles + rounds - 1) / rounds};
+    }
+  }
+  return best;
+}
+template <int NB>
+nvq_status launch_w4a16_tmem(nvq::w4a16_tmem::Params p, TmemSplit split, cudaStream_t stream) {
+  using namespace nvq::w4a16_tmem;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t err[kMaxDevices];
+  const nvq_status st = kernel_opt_in(gemm_kernel<NB>, Cfg<NB>::SMEM, false, once, err, "w4a16_gemm_epilogue: smem attribute");
+  if (st != NVQ_OK) return st;
+  p.slog = split.slog;
+  p.slices = 1u << split.slog;
+  return launch_dependent("w4a16_gemm_epilogue", gemm_kernel<NB>, (int)(split.clusters * p.slices), THREADS, Cfg<NB>::SMEM,
+                          (int)p.slices, stream, p);
 }
 
 // Workspace of nvq_linear's W4A4 path: activation codes, tiled scales, t and
@@ -742,8 +781,21 @@ nvq_status w4a16_gemm_epilogue(const void* x_bf16, const uint8_t* packed_codes, 
   if (spans_meet(bf16_span(x_bf16, M, K, K), bf16_span(y_bf16, M, N, (int64_t)ep.ldy)))
     return fail(NVQ_ERR_INVALID_ARG, "w4a16_gemm_epilogue: x overlaps y");
   if (M <= 8) return launch_w4a16<1, false, true>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream, ep);
-  if (M <= 16) return launch_w4a16<2, false, true>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream, ep);
-  return launch_w4a16<4, false, true>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream, ep);
+  const TmemSplit split = w4a16_tmem_split(M, N, K, M <= 16 ? 16 : 32);
+  // Up to 16 rows, where the tiles fill less than 4/5 of their rounds over the SMs, the
+  // streaming kernel, which cuts finer, is faster.
+  if (M <= 16 && split.rounds > 1 && split.clusters * 5 < (148ull >> split.slog) * 4)
+    return launch_w4a16<2, false, true>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream, ep);
+  nvq::w4a16_tmem::Params p = {};
+  p.x = static_cast<const __nv_bfloat16*>(x_bf16);
+  p.codes = packed_codes;
+  p.scales = static_cast<const uint8_t*>(packed_scales);
+  p.y = static_cast<__nv_bfloat16*>(y_bf16);
+  p.M = (uint32_t)M;
+  p.N = (uint32_t)N;
+  p.K = (uint32_t)K;
+  p.ep = ep;
+  return M <= 16 ? launch_w4a16_tmem<16>(p, split, stream) : launch_w4a16_tmem<32>(p, split, stream);
 }
 
 // ------------------------------------------------------------------ 2:4 sparse INT4 decode

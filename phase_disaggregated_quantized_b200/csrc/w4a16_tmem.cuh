@@ -1,0 +1,426 @@
+// W4A16 decode GEMM with an epilogue for more than 8 rows of X, on the tcgen05 tensor
+// cores with the dequantized weights in TMEM.
+//
+//   Y[m, n] = act( sum_g s[n, g] sum_{k in g} X[m, k] (u[n, k] - 8) + bias[n] ) + residual[m, n]
+//
+// The 128 lanes of TMEM are the weight rows of a tile (four packed units of 32 rows), the
+// MMA's N is 16 or 32 rows of X, its K one group of 128.  So X is read once per 128
+// weight rows; the warp-level MMAs of the streaming kernel re-read it per 32 and issue
+// four products per fragment for 32 rows.
+//
+//   warps 0..15   dequantize: warp w has lanes 32 (w % 4) .. and the groups i of set
+//                 w / 4 = i % 4.  Its units arrive in a shared-memory ring of its own
+//                 (cp.async); nibbles become (u - 8) / 4 in BF16 (exact) and go to TMEM
+//                 in the order in which the packed form has them, that of a 16 x 16 MMA
+//                 fragment, which is what tcgen05.st.16x256b writes.  While the next
+//                 group of the set is multiplied, the sums of the last one are read
+//                 back, a row per lane, and s times them added to the row's FP32 sums.
+//   warps 16..19  one per set: the set's groups of X into two 128-byte-swizzled buffers
+//                 (through registers: the packed order of k is not one that a bulk copy
+//                 could write) and, per group, eight 128 x N x 16 MMAs, A from TMEM.
+//
+// `full` (a set's four warps stored) and `done` (its MMAs are complete) are the only
+// hand-offs: a set stores group i after `done` of group i - 4, so when group i is full
+// the operands of group i - 4 are free, and the sums of group i - 8 have been read.
+// A tile's k-groups are cut over the CTAs of a cluster, their sums meet in shared memory
+// across it and each CTA finishes a share of the rows; sums are added in a fixed order.
+//
+// Measured (32 rows; the streaming kernel in brackets): N K 4096 12288: 16.2 us (26.1),
+// 4096 4096: 9.5 (15.5), 1024 8192: 9.9 (15.2), 16384 4096: 18.2 (29.5), 24576 4096: 33.1
+// (40.2); 16 rows: 13.0 (15.0), 7.8 (8.6), -, 18944 4096: 15.3 (19.4).  An MMA takes 45
+// cycles issued alone, whatever N up to 64, 75 to 100 here; a group 560 cycles for 16 rows
+// and 740 for 32, in which the ALUs (80 instructions per unit for the nibbles) are half
+// busy.  With two sets and one MMA warp a group took 1700 cycles: that warp's waits and
+// commits are not free.  What is left is the chain MMAs -> `done` -> dequantize -> `full`
+// and, for large N, rounds of tiles that do not fill the SMs.
+#pragma once
+#include <cuda_bf16.h>
+#include "epilogue.cuh"
+#include "ptx.cuh"
+#include "w4a16_gemm.cuh"
+
+namespace nvq {
+namespace w4a16_tmem {
+
+constexpr uint32_t ROWS = 128;                // weight rows of a tile
+constexpr uint32_t STAGES = 4;                // sets of four dequantizing warps, A stages in TMEM, groups of X
+constexpr uint32_t DSTAGES = 2 * STAGES, XSTAGES = 2 * STAGES;   // sums in TMEM, groups of X in shared memory
+constexpr int DWARPS = 4 * STAGES;
+constexpr int THREADS = (DWARPS + STAGES) * 32;
+constexpr uint32_t DTHREADS = DWARPS * 32;
+constexpr int RING = 3;                       // units in flight per warp
+constexpr uint32_t SLOT = 2048 + 64;          // codes, scales
+constexpr uint32_t PSTRIDE = ROWS + 4;        // floats of a token's partial sums
+constexpr uint32_t TMEM_COLS = 512, A_COLS = 64, D_COL0 = STAGES * A_COLS;
+
+template <int NB>                             // rows of X per tile: 16 or 32
+struct Cfg {
+  static constexpr uint32_t ATOM = NB * 128;  // 64 k of NB rows
+  static constexpr uint32_t XSTAGE = 2 * ATOM;
+  static constexpr uint32_t OFF_RING = XSTAGES * XSTAGE;
+  static constexpr uint32_t OFF_PART = OFF_RING + DWARPS * RING * SLOT;
+  static constexpr uint32_t OFF_BAR = OFF_PART + 2 * NB * PSTRIDE * 4;
+  static constexpr uint32_t NUM_BARS = 3 * STAGES;   // full, done, drain
+  static constexpr int SMEM = (int)(OFF_BAR + NUM_BARS * 8 + 16 + 1024);   // + slack for 1024-byte alignment
+  // kind::f16: FP32 sums, A and B BF16, both K-major.
+  static constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(NB >> 3) << 17) | ((ROWS >> 4) << 24);
+  static_assert(ATOM % 1024 == 0 && OFF_RING % 16 == 0 && OFF_PART % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+  static_assert(SMEM <= 232448 && D_COL0 + DSTAGES * NB <= TMEM_COLS, "shared memory, TMEM");
+};
+
+struct Params {
+  const __nv_bfloat16* x;                     // [M, K]
+  const uint8_t* codes;
+  const uint8_t* scales;
+  __nv_bfloat16* y;
+  uint32_t M, N, K, slices, slog;             // slices = 2^slog CTAs of a cluster
+  EpiParams ep;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The eight nibbles u of a packed word as BF16 (u - 8) / 4, in the order that
+// tcgen05.st.16x256b wants (rows g, g, g + 8, g + 8).  Nibble 0 of a half word becomes
+// 128 + u through the exponent bits; nibble 1, in place, is the BF16 subnormal (or smallest
+// normal) 16 u 2^-133, which 2^127 makes u / 4: a shift less than one of its own.  Both
+// products and sums are exact.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ void quarter_values(uint32_t w, uint32_t* a) {
+  constexpr uint32_t kQuarter = 0x3E803E80u, kNeg34 = 0xC208C208u, k2p127 = 0x7F007F00u, kNeg2 = 0xC000C000u;
+  const uint32_t w8 = w4a16::shr32(w, 8);
+  a[0] = fma_bf16x2(w4a16::nibbles_to_bf16x2(w), kQuarter, kNeg34);     // nibbles 0: row g, first k pair
+  a[2] = fma_bf16x2(w & 0x00F000F0u, k2p127, kNeg2);                     // 1: row g + 8
+  a[1] = fma_bf16x2(w4a16::nibbles_to_bf16x2(w8), kQuarter, kNeg34);    // 2: row g, second k pair
+  a[3] = fma_bf16x2(w8 & 0x00F000F0u, k2p127, kNeg2);                    // 3: row g + 8
+}
+
+template <int NB>
+__global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
+  using C = Cfg<NB>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_addr(smem);
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+  const uint32_t full = sbase + C::OFF_BAR, done = full + 8 * STAGES, drain_bar = done + 8 * STAGES;
+  uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * C::NUM_BARS);
+  const uint32_t G = p.K >> 7, rank = w4a16::cluster_rank(), cid = w4a16::cluster_id(), nclu = w4a16::cluster_count();
+  const uint32_t k0 = (uint32_t)((uint64_t)G * rank >> p.slog), nk = (uint32_t)((uint64_t)G * (rank + 1) >> p.slog) - k0;   // >= 1
+  const uint32_t ntile = (p.N + ROWS - 1) / ROWS, tiles = ntile * ((p.M + NB - 1) / NB), utiles = p.N >> 5;
+
+  // ---- dequantizing warps: the units of this warp, in the order of its groups
+  const uint32_t q = warp & 3u, set = warp >> 2;
+  const uint32_t ring = sbase + C::OFF_RING + warp * RING * SLOT;
+  uint32_t rtile = cid, rk = set, rslot = ring + 16 * lane, rn = 0;
+  const uint8_t *rcodes = nullptr, *rscales = nullptr;
+  bool rvalid = false;
+  auto locate = [&]() {                       // from group rk of tile rtile on, which may lie past the tile's end
+    while (rk >= nk) {
+      rk -= nk;
+      rtile += nclu;
+    }
+    const uint32_t u = 4 * (rtile % ntile) + q;
+    rvalid = rtile < tiles && u < utiles;
+    const size_t unit = (size_t)u * G + k0 + rk;
+    rcodes = p.codes + unit * 2048 + 16 * lane;
+    rscales = p.scales + unit * 64 + 16 * lane;
+  };
+  auto request = [&]() {
+    if (rvalid) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cp_async16(rslot + 512 * i, rcodes + 512 * i);
+      if (lane < 4) cp_async16(rslot + 2048, rscales);
+    }
+    cp_commit();
+    rslot += SLOT;
+    if (++rn == RING) {
+      rn = 0;
+      rslot -= RING * SLOT;
+    }
+    rcodes += STAGES * 2048;
+    rscales += STAGES * 64;
+    if ((rk += STAGES) >= nk) locate();
+  };
+  if (warp < DWARPS) {                        // constant inputs: requested while the kernel before ends
+    locate();
+#pragma unroll 1
+    for (int i = 0; i < RING; ++i) request();
+  }
+  if (threadIdx.x == DTHREADS) {
+    for (uint32_t s = 0; s < STAGES; ++s) {
+      mbar_init(full + 8 * s, 4);             // the warps of a set
+      mbar_init(done + 8 * s, 1);
+      mbar_init(drain_bar + 8 * s, 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == DWARPS) {
+    __syncwarp();
+    tmem_alloc(smem_addr(tmem_ptr), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_ptr;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  bool ok = true;
+  if (warp < DWARPS) {
+    float* part = reinterpret_cast<float*>(smem + C::OFF_PART);           // [set mod 2][token][row]
+    uint32_t slot = ring;
+    const uint32_t row = q * 32 + lane, lanes = (q * 32u) << 16;
+    // bf16 scales of row r of a unit at 4 (r % 8) + 2 (r / 16) + (r / 8) % 2.
+    const uint32_t s_at = 2048 + 2 * (4 * (lane & 7u) + 2 * (lane >> 4) + ((lane >> 3) & 1u));
+    float acc[NB];                                                        // a quarter of the sums of tile `summed`
+#pragma unroll
+    for (int t = 0; t < NB; ++t) acc[t] = 0.f;
+    uint32_t summed = cid;
+    auto has_rows = [&](uint32_t tile) { return 4 * (tile % ntile) + q < utiles; };
+    bool sum_valid = has_rows(cid);
+    auto wait_done = [&](uint32_t i) {
+      if (ok) ok = warp_mbar_wait(done + 8 * set, (i / STAGES) & 1u);
+    };
+    auto drain = [&](uint32_t i, float scale) {                           // the sums of group i
+      if (!sum_valid) return;
+      tc_fence_after();
+#pragma unroll
+      for (int t0 = 0; t0 < NB; t0 += 16) {
+        uint32_t v[16];
+        tc_ld_32x32b_x16(tmem + lanes + D_COL0 + NB * (i & (DSTAGES - 1)) + t0, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int t = 0; t < 16; ++t) acc[t0 + t] = __fmaf_rn(scale, __uint_as_float(v[t]), acc[t0 + t]);
+      }
+    };
+    // Finishes tile `summed`: every warp's sums, then four rows of one token for each of this thread's outputs.
+    auto finish = [&]() {
+      const uint32_t mb = summed / ntile, nt = summed - mb * ntile;
+      const uint32_t rows = ROWS >> p.slog, qlog = 5 - p.slog, items = NB << qlog;
+      constexpr int ITEMS = NB * 32 / DTHREADS;
+      auto output = [&](uint32_t it, uint32_t& t, uint32_t& r, uint32_t& m, uint32_t& n) {
+        t = it >> qlog;
+        r = rank * rows + 4 * (it & ((1u << qlog) - 1));
+        m = mb * NB + t;
+        n = nt * ROWS + r;
+        return it < items && m < p.M && n < p.N;
+      };
+      uint2 res[ITEMS] = {};
+      uint32_t t, r, m, n;
+      if (p.ep.residual != nullptr)
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j)
+          if (output(threadIdx.x + j * DTHREADS, t, r, m, n))
+            res[j] = *reinterpret_cast<const uint2*>(p.ep.residual + (size_t)m * p.ep.ldr + n);
+      if (p.slices > 1 && summed != cid) {
+        __syncwarp();
+        w4a16::cluster_wait();                                            // the other CTAs have read the last tile's sums
+      }
+      float* mine = part + (set & 1u) * NB * PSTRIDE + row;
+      if (set >= 2)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) mine[j * PSTRIDE] = acc[j];
+      named_barrier_sync(1, DTHREADS);
+      if (set < 2)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) mine[j * PSTRIDE] += acc[j];
+      if (p.slices > 1) {
+        __syncwarp();
+        w4a16::cluster_arrive();
+        w4a16::cluster_wait();
+      } else {
+        named_barrier_sync(1, DTHREADS);
+      }
+      const uint32_t after = w4a16::after_cluster_wait();
+#pragma unroll
+      for (int j = 0; j < ITEMS; ++j)
+        if (output(threadIdx.x + j * DTHREADS, t, r, m, n)) {
+          const uint32_t at = sbase + C::OFF_PART + (t * PSTRIDE + r) * 4;
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+          for (uint32_t k = 0; k < p.slices; ++k) {
+            float4 f[2];
+#pragma unroll
+            for (uint32_t z = 0; z < 2; ++z) f[z] = w4a16::ld_cluster_f32x4(at + z * NB * PSTRIDE * 4, k, after);
+#pragma unroll
+            for (uint32_t z = 0; z < 2; ++z) {
+              v[0] += f[z].x; v[1] += f[z].y; v[2] += f[z].z; v[3] += f[z].w;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] *= 4.f;
+          if (p.ep.bias != nullptr) {
+            const uint2 b = *reinterpret_cast<const uint2*>(p.ep.bias + n);
+            v[0] += bf16_lo(b.x); v[1] += bf16_hi(b.x); v[2] += bf16_lo(b.y); v[3] += bf16_hi(b.y);
+          }
+          activate(v, p.ep.act);
+          if (p.ep.residual != nullptr) {
+            v[0] += bf16_lo(res[j].x); v[1] += bf16_hi(res[j].x); v[2] += bf16_lo(res[j].y); v[3] += bf16_hi(res[j].y);
+          }
+          *reinterpret_cast<uint2*>(p.y + (size_t)m * p.ep.ldy + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        }
+      if (p.slices > 1) {
+        __syncwarp();
+        w4a16::cluster_arrive();
+      } else {
+        named_barrier_sync(1, DTHREADS);
+      }
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[j] = 0.f;
+      summed += nclu;
+      sum_valid = has_rows(summed);
+    };
+
+    float before = 0.f;                                                   // scale of this set's group before, whose sums are still in TMEM
+    uint32_t i = set, k = set, tile = cid;                                // this set's next group: k of `tile`
+    bool valid = sum_valid;
+    for (;; i += STAGES, k += STAGES) {
+      if (k >= nk) {
+        while (k >= nk) {
+          k -= nk;
+          tile += nclu;
+        }
+        valid = has_rows(tile);
+      }
+      if (tile >= tiles) break;
+      cp_wait<RING - 1>();
+      __syncwarp();                                                       // the scales came through other lanes
+      float scale = 0.f;
+      if (valid) {
+        uint16_t s16;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(s16) : "r"(slot + s_at));
+        scale = __uint_as_float((uint32_t)s16 << 16);
+      }
+      if (i >= STAGES) wait_done(i - STAGES);
+      if (valid) {
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 w[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) w[j] = w4a16::lds128(slot + 16 * lane + 1024 * h + 512 * j);
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt) {
+            uint32_t a[16];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint4 v = w[j >> 1];
+              quarter_values(tt ? ((j & 1) ? v.w : v.y) : ((j & 1) ? v.z : v.x), a + 4 * j);
+            }
+            tc_st_16x256b_x4(tmem + lanes + ((16u * tt) << 16) + A_COLS * set + 32 * h, a);
+          }
+        }
+        tc_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * set);
+      request();
+      slot = slot == ring + (RING - 1) * SLOT ? ring : slot + SLOT;
+      if (i >= STAGES) drain(i - STAGES, before);
+      before = scale;
+      while (summed != tile) finish();                                    // with the next tile's first group under way
+    }
+    if (i >= STAGES) {                                                    // the last group of this set
+      wait_done(i - STAGES);
+      drain(i - STAGES, before);
+    }
+    while (summed < tiles) finish();
+    if (p.slices > 1) w4a16::cluster_wait();                              // nobody reads this CTA's sums any more
+  } else {
+    // Stage st: X of groups st, st + 4, ... and their MMAs.  A lane loads k 8 u .. 8 u + 7 of
+    // rows 2 r + half, a group of its own ahead; k = 32 c + 4 j + e is column 16 j + 4 c + e
+    // of the stage, so the two halves (j = 2 (u % 4) and the next) lie 32 bytes apart.
+    const uint32_t st = warp - DWARPS, half = lane >> 4, u = lane & 15u, c = u >> 2;
+    const uint32_t chunk = 4 * (u & 1u) + (c >> 1), to = sbase + 2 * st * C::XSTAGE + ((u & 3u) >> 1) * C::ATOM + half * 128 + 8 * (c & 1u);
+    const uint32_t swz[2] = {(chunk ^ half) << 4, ((chunk + 2) ^ half) << 4};
+    const uint64_t bdesc = smem_desc(sbase + 2 * st * C::XSTAGE, 0, 1024, kSwizzle128B);
+    const uint32_t row_bytes = 2 * p.K;                                  // 32 rows of them fit in 32 bits
+    uint4 v[NB / 2] = {};
+    uint32_t xtile = cid, xk = st;                                        // the next group loaded
+    auto load = [&]() {
+      while (xk >= nk) {
+        xk -= nk;
+        xtile += nclu;
+      }
+      if (xtile >= tiles) return;
+      const uint32_t m0 = xtile / ntile * NB, last = min((uint32_t)NB, p.M - m0) - 1;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.x + (size_t)m0 * p.K + (size_t)(k0 + xk) * 128) + 16 * u;
+#pragma unroll
+      for (uint32_t r = 0; r < NB / 2; ++r)                               // past M: the last row again, for sums that are dropped
+        v[r] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)min(2 * r + half, last) * row_bytes));
+      xk += STAGES;
+    };
+    auto store = [&](uint32_t buf) {
+#pragma unroll
+      for (uint32_t r = 0; r < NB / 2; ++r) {
+        const uint32_t o = to + buf * C::XSTAGE + r * 256, x = (2 * (r & 3u)) << 4;
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(o + (swz[0] ^ x)), "r"(v[r].x), "r"(v[r].y) : "memory");
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(o + (swz[1] ^ x)), "r"(v[r].z), "r"(v[r].w) : "memory");
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    load();
+    store(0);
+    load();
+    uint32_t i = st, end = nk, buf = 0;
+    for (uint32_t tile = cid; tile < tiles; tile += nclu, end += nk) {
+#pragma unroll 1
+      for (; i < end; i += STAGES, buf ^= 1u) {
+        if (lane == 0) {
+          if (ok) ok = mbar_wait(full + 8 * st, (i / STAGES) & 1u);
+          if (ok) {
+            tc_fence_after();
+            const uint64_t bd = bdesc + buf * (C::XSTAGE >> 4);
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)
+              tc_mma_bf16_ts(tmem + D_COL0 + NB * (i & (DSTAGES - 1)), tmem + A_COLS * st + 8 * j, bd + (j >> 2) * (C::ATOM >> 4) + 2 * (j & 3u),
+                             C::IDESC, j != 0);
+            tc_commit(done + 8 * st);
+          }
+        }
+        __syncwarp();
+        // The other buffer's group i - 4 is done: the warps that stored group i waited for it.
+        store(buf ^ 1u);
+        load();
+      }
+      if (p.slices > 1) {                                                 // this warp's part in the cluster's barriers, a tile behind
+        if (tile != cid) {
+          w4a16::cluster_wait();
+          w4a16::cluster_arrive();
+          w4a16::cluster_wait();
+        }
+        w4a16::cluster_arrive();
+      }
+    }
+    if (p.slices > 1) {
+      w4a16::cluster_wait();
+      w4a16::cluster_arrive();
+      w4a16::cluster_wait();
+    }
+    if (lane == 0) {                                                      // every MMA has finished before TMEM is released
+      tc_commit(drain_bar + 8 * st);
+      mbar_wait_drain(drain_bar + 8 * st, 0, 200000000ull);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == DWARPS) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+}  // namespace w4a16_tmem
+}  // namespace nvq

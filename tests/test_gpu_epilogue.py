@@ -83,7 +83,9 @@ def _cu(t):
 
 
 INT4_SHAPES = [(1, 32, 128), (1, 4096, 256), (7, 96, 384), (8, 2080, 1152), (9, 64, 128), (16, 352, 4096),
-               (17, 32, 256), (32, 1056, 384), (33, 96, 128), (70, 64, 640)]
+               (17, 32, 256), (32, 1056, 384), (33, 96, 128), (70, 64, 640),
+               # more than 8 rows: k-groups cut over 8, 4 or 2 CTAs, several rounds of tiles, tiles of one group
+               (12, 64, 8192), (20, 96, 1152), (13, 2080, 2048), (25, 8224, 1024), (16, 18976, 128), (24, 19104, 640), (320, 1920, 6144)]
 NVFP4_SHAPES = [(1, 8, 64), (5, 264, 128), (31, 72, 192), (128, 256, 256), (129, 520, 1088), (300, 1000, 320),
                 (1030, 2312, 64),
                 # few tiles, whose k-stages 8, 4 or 2 CTAs split
@@ -105,7 +107,7 @@ def test_every_epilogue_matches_the_oracle(form, shape):
 
 @pytest.mark.parametrize("form", [Int4, Nvfp4])
 def test_empty_epilogue_is_the_bare_product_bit_for_bit(form):
-    x, w, _, _ = _draw(24, 160, 512, seed=3)
+    x, w, _, _ = _draw(6 if form is Int4 else 24, 160, 512, seed=3)
     op = form(x, w)
     assert torch.equal(op(), op.bare())
 
@@ -161,6 +163,36 @@ def test_values_that_are_not_finite_stay_where_they_are(form):
     for act in oepi.ACTIVATIONS:
         y = op(bias=bias.cuda(), activation=act).float().cpu()
         assert torch.isnan(y[:, 11]).all() and torch.isfinite(y[:, :11]).all() and torch.isfinite(y[:, 12:]).all()
+
+
+@pytest.mark.parametrize("M, N, K", [(9, 96, 256), (16, 160, 1152), (17, 96, 256), (32, 288, 2048), (45, 64, 640)])
+def test_int4_sums_of_integers_are_exact(M, N, K):
+    """Integer x, every code, power-of-two scales: the FP32 sums hold the result exactly, y is its one rounding."""
+    g = torch.Generator().manual_seed(M)
+    x = torch.randint(-8, 9, (M, K), generator=g).to(torch.bfloat16)
+    u = torch.randint(0, 16, (N, K), generator=g, dtype=torch.uint8)
+    s = torch.exp2(torch.randint(-2, 3, (N, K // 128), generator=g).float()).to(torch.bfloat16)
+    packed = nvq.int4_pack_weights((u[:, 0::2] | (u[:, 1::2] << 4)).cuda(), s.cuda(), N, K)
+    y = nvq.w4a16_gemm_epilogue(x.cuda(), *packed, N)
+    w = (u.double() - 8) * s.double().repeat_interleave(128, 1)
+    want = x.double() @ w.T                                 # |sums| < 2^21, multiples of 2^-2
+    assert torch.equal(y.cpu(), want.float().to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("M", [9, 16, 19, 31, 50])
+def test_rows_do_not_see_one_another(M):
+    """A row of NaN, and NaN behind the last row, change nothing but that row."""
+    x, w, bias, _ = _draw(M, 160, 1024, seed=M)
+    op = Int4(x, w)
+    want = op(bias=bias.cuda())
+    wide = torch.full((M + 70, 1024), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:M] = op.x
+    wide[3] = float("nan")
+    op.x = wide[:M]
+    y = op(bias=bias.cuda())
+    assert torch.isnan(y[3]).all()
+    y[3] = want[3]
+    assert torch.equal(y, want)
 
 
 @pytest.mark.parametrize("act", oepi.ACTIVATIONS)
@@ -224,7 +256,8 @@ def test_phase_dispatch_takes_the_epilogue_along(M):
     assert torch.equal(got, i4(**kw) if M <= nvq.default_crossover_m() else f4(**kw))
     assert torch.equal(nvq.nvq_linear_epilogue(x.cuda(), f4.w, None, 160, crossover_m=0, **kw), f4(**kw))
     assert torch.equal(nvq.nvq_linear_epilogue(x.cuda(), None, i4.w, 160, crossover_m=10 ** 6, **kw), i4(**kw))
-    assert torch.equal(nvq.nvq_linear_epilogue(x.cuda(), f4.w, i4.w, 160), nvq.nvq_linear(x.cuda(), f4.w, i4.w, 160))
+    if not 8 < M <= nvq.default_crossover_m():              # there the INT4 product has sums in an order of its own
+        assert torch.equal(nvq.nvq_linear_epilogue(x.cuda(), f4.w, i4.w, 160), nvq.nvq_linear(x.cuda(), f4.w, i4.w, 160))
 
 
 def test_binding_refusals():
