@@ -529,56 +529,26 @@ struct Weights {                    // one unit's codes of this lane and its fou
   }
 };
 
-constexpr uint32_t kNeg136 = 0xC308C308u;                // bf16x2 (-136, -136)
-
-// -136 times the sum of each column: off[0] for column 2 c, off[1] for 2 c + 1.
-__device__ __forceinline__ void column_offsets(const uint4 (&b)[4], float (&off)[2]) {
-  const uint32_t neg[4] = {kNeg136, kNeg136, kNeg136, kNeg136};
-  float d[4];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint4 q = b[j >> 1];
-    const uint32_t b0 = (j & 1) ? q.z : q.x, b1 = (j & 1) ? q.w : q.y;
-    if (j == 0) w4a16::mma_z(d, neg, b0, b1);
-    else w4a16::mma_acc(d, neg, b0, b1);
-  }
-  off[0] = d[0];
-  off[1] = d[1];
-}
-
-// acc[n][tt] += scale * (sum of the unit's codes times the columns b[n] - 8 times their
-// sum).  The codes enter as 128 + u; what that adds is taken off by `off` (GIVEN:
-// column_offsets of b[n], the first products' C operand) or by a third chain of products
-// next to those of the two row tiles, whose latency it shares.
-template <bool GIVEN, int NB>
-__device__ __forceinline__ void unit_products(const Weights& w, const uint4 (&b)[NB][4], const float (&off)[NB][2],
-                                              float (&acc)[NB][2][4]) {
-  const uint32_t neg[4] = {kNeg136, kNeg136, kNeg136, kNeg136};
-  float o[NB][4], d[NB][2][4];
+// acc[n][tt] += scale / 4 * (the unit's rows of tile tt times the columns b[n]).
+template <int NB>
+__device__ __forceinline__ void unit_products(const Weights& w, const uint4 (&b)[NB][4], float (&acc)[NB][2][4]) {
+  float d[NB][2][4];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint4 v = w.q[j >> 1];
     uint32_t a0[4], a1[4];
-    w4a16::word_to_frag((j & 1) ? v.z : v.x, a0);
-    w4a16::word_to_frag((j & 1) ? v.w : v.y, a1);
+    w4a16::word_to_quarters((j & 1) ? v.z : v.x, a0);
+    w4a16::word_to_quarters((j & 1) ? v.w : v.y, a1);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const uint4 q = b[n][j >> 1];
       const uint32_t b0 = (j & 1) ? q.z : q.x, b1 = (j & 1) ? q.w : q.y;
       if (j == 0) {
-        if constexpr (GIVEN) {
-          const float c[4] = {off[n][0], off[n][1], off[n][0], off[n][1]};
-          w4a16::mma_c(d[n][0], a0, b0, b1, c);
-          w4a16::mma_c(d[n][1], a1, b0, b1, c);
-        } else {
-          w4a16::mma_z(d[n][0], a0, b0, b1);
-          w4a16::mma_z(d[n][1], a1, b0, b1);
-          w4a16::mma_z(o[n], neg, b0, b1);
-        }
+        w4a16::mma_z(d[n][0], a0, b0, b1);
+        w4a16::mma_z(d[n][1], a1, b0, b1);
       } else {
         w4a16::mma_acc(d[n][0], a0, b0, b1);
         w4a16::mma_acc(d[n][1], a1, b0, b1);
-        if constexpr (!GIVEN) w4a16::mma_acc(o[n], neg, b0, b1);
       }
     }
   }
@@ -588,38 +558,31 @@ __device__ __forceinline__ void unit_products(const Weights& w, const uint4 (&b)
 #pragma unroll
     for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[n][tt][i] = __fmaf_rn(sc[2 * tt + (i >> 1)], GIVEN ? d[n][tt][i] : d[n][tt][i] + o[n][i], acc[n][tt][i]);
+      for (int i = 0; i < 4; ++i) acc[n][tt][i] = __fmaf_rn(sc[2 * tt + (i >> 1)], d[n][tt][i], acc[n][tt][i]);
 }
 
-// The same for one of the unit's two row tiles (tt), the third chain included.
+// The same for one of the unit's two row tiles (tt).
 template <int NB>
 __device__ __forceinline__ void half_products(const Weights& w, uint32_t tt, const uint4 (&b)[NB][4], float (&acc)[NB][2][4]) {
-  const uint32_t neg[4] = {kNeg136, kNeg136, kNeg136, kNeg136};
-  float o[NB][4], d[NB][4];
+  float d[NB][4];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint4 v = w.q[j >> 1];
     uint32_t a[4];
-    w4a16::word_to_frag((j & 1) ? (tt ? v.w : v.z) : (tt ? v.y : v.x), a);
+    w4a16::word_to_quarters((j & 1) ? (tt ? v.w : v.z) : (tt ? v.y : v.x), a);
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const uint4 q = b[n][j >> 1];
       const uint32_t b0 = (j & 1) ? q.z : q.x, b1 = (j & 1) ? q.w : q.y;
-      if (j == 0) {
-        w4a16::mma_z(d[n], a, b0, b1);
-        w4a16::mma_z(o[n], neg, b0, b1);
-      } else {
-        w4a16::mma_acc(d[n], a, b0, b1);
-        w4a16::mma_acc(o[n], neg, b0, b1);
-      }
+      if (j == 0) w4a16::mma_z(d[n], a, b0, b1);
+      else w4a16::mma_acc(d[n], a, b0, b1);
     }
   }
   const uint32_t s = tt ? w.s.y : w.s.x;
 #pragma unroll
   for (int n = 0; n < NB; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[n][0][i] = __fmaf_rn((i & 2) ? bf16_hi(s) : bf16_lo(s), d[n][i] + o[n][i], acc[n][0][i]);
+    for (int i = 0; i < 4; ++i) acc[n][0][i] = __fmaf_rn((i & 2) ? bf16_hi(s) : bf16_lo(s), d[n][i], acc[n][0][i]);
 }
 
 // h is kept in the order in which the down phase reads it: inside a group of 128
@@ -643,15 +606,14 @@ __device__ __forceinline__ uint32_t ticket(uint32_t* counter) {
 // ------------------------------------------------------------------ the layer
 constexpr int RING = 3;
 // Shared memory behind the ring.  Gate and up: the cut tiles (two of 16 x 8 x 2 sums
-// per warp) and the column offsets of up to kOffsets (segment, group) pairs.  Down: the
+// per warp).  Down: the
 // per-token rows of each warp and, where it fits with them, all of h (P pairs of I
 // values, two halves each): a few tokens' h, which every CTA reads whole.
-constexpr uint32_t kOffsets = 512;
 template <int W>
 struct Smem {
   static constexpr int RING_BYTES = W * RING * SLOT;
   static constexpr int CUT_TILES = W * 2 * 1024;
-  static constexpr int GATE_UP = RING_BYTES + CUT_TILES + (int)kOffsets * 32;
+  static constexpr int GATE_UP = RING_BYTES + CUT_TILES;
   static constexpr int BEHIND_RING = W == 8 ? 40 * 1024 : 64 * 1024;
   static constexpr bool stage_h(int64_t T, int64_t P, int64_t I) { return W * T * 32 * 4 + P * I * 4 <= BEHIND_RING; }
   static constexpr int down(int64_t T, int64_t P, int64_t I) {
@@ -757,7 +719,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) gate_up_kernel(const ExpertPar
           __nv_bfloat16* to = p.h + (size_t)pr * I + h_at(rt) + g8;
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float gate = acc[0][2 * r + k], h = times_sigmoid(gate, gate) * acc[1][2 * r + k] * w;
+            const float gate = 4.f * acc[0][2 * r + k], up = 4.f * acc[1][2 * r + k], h = times_sigmoid(gate, gate) * up * w;
             // Two BF16 halves carry h to 16 bits: one would add an error as large as the rounding of y.
             const __nv_bfloat16 hi = __float2bfloat16_rn(h);
             to[32 * r] = hi;
@@ -798,67 +760,37 @@ __global__ void __launch_bounds__(W * 32, 16 / W) gate_up_kernel(const ExpertPar
 #pragma unroll
       for (int i = 0; i < 4; ++i) b[i] = __ldg(row + at * 16 + i);
     };
-    // While the first weights are on their way: the column offsets of this CTA's
-    // segments, which each of their row tiles needs again.
-    const uint32_t seg0 = p.by_rtiles.div(T0), nseg = mine ? p.by_rtiles.div(T0 + mine - 1) - seg0 + 1 : 0u;
-    const bool given = nseg * G <= kOffsets;
-    float2* offsets = reinterpret_cast<float2*>(esm + S::RING_BYTES + S::CUT_TILES);   // [segment][group][c]
-    if (given) {
-#pragma unroll 2
-      for (uint32_t i = warp; i < nseg * G; i += W) {
-        const uint32_t s = p.by_g.div(i);
-        uint4 b[4];
-        float off[2];
-        load_x(row_of(seg0 + s), i - s * G, b);
-        column_offsets(b, off);
-        if (g8 == 0) offsets[i * 4 + c] = make_float2(off[0], off[1]);
-      }
-      __syncthreads();
-    }
     if (any) {
       const uint4* row = row_of(seg);
-      const float2* offs = offsets + (seg - seg0) * G * 4 + c;
       uint4 xv[1][4];
       load_x(row, g, xv[0]);
       float acc[1][2][4] = {};
       bool head = g != 0;                                              // the first tile began in another run
-      auto run = [&](auto tab) {
-        constexpr bool GIVEN = decltype(tab)::value;
 #pragma unroll 1
-        for (uint32_t f = f0; f < f1; ++f) {
-          float off[1][2] = {};
-          if constexpr (GIVEN) {
-            const float2 o = offs[g * 4];
-            off[0][0] = o.x;
-            off[0][1] = o.y;
-          }
-          cp_wait<RING - 1>();
-          Weights w;
-          w.read(ring.at, lane);
-          unit_products<GIVEN, 1>(w, xv, off, acc);
-          const uint32_t oseg = seg, ort = rt;
-          const bool ends = ++g == G;
-          if (ends) {
-            g = 0;
-            if (++rt == rtiles) {
-              rt = 0;
-              if (++seg < segments) row = row_of(seg);
-              offs += G * 4;
-            }
-          }
-          if (f + 1 < f1) load_x(row, g, xv[0]);
-          fill();
-          if (ends) {
-            if (head) put(acc[0], 0);
-            else finish(acc[0], oseg, ort);
-            head = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[0][0][i] = acc[0][1][i] = 0.f;
+      for (uint32_t f = f0; f < f1; ++f) {
+        cp_wait<RING - 1>();
+        Weights w;
+        w.read(ring.at, lane);
+        unit_products<1>(w, xv, acc);
+        const uint32_t oseg = seg, ort = rt;
+        const bool ends = ++g == G;
+        if (ends) {
+          g = 0;
+          if (++rt == rtiles) {
+            rt = 0;
+            if (++seg < segments) row = row_of(seg);
           }
         }
-      };
-      if (given) run(std::true_type());
-      else run(std::false_type());
+        if (f + 1 < f1) load_x(row, g, xv[0]);
+        fill();
+        if (ends) {
+          if (head) put(acc[0], 0);
+          else finish(acc[0], oseg, ort);
+          head = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[0][0][i] = acc[0][1][i] = 0.f;
+        }
+      }
       if (g != 0) put(acc[0], first == p.by_g.div(f1 - 1) ? 0 : 1);    // the run ends inside a tile
     }
     __syncthreads();
@@ -966,7 +898,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) down_kernel(const ExpertParams
       }
   };
   auto store = [&](uint32_t n, uint32_t i, float v, uint16_t r) {
-    p.y[output_at(n, i)] = __float2bfloat16_rn(v + __uint_as_float((uint32_t)r << 16));   // r = 0 without a residual
+    p.y[output_at(n, i)] = __float2bfloat16_rn(__fmaf_rn(4.f, v, __uint_as_float((uint32_t)r << 16)));   // r = 0 without a residual
   };
   auto clear_rows = [&]() {
     for (uint32_t i = lane; i < outs; i += 32) rows[i] = 0.f;
@@ -1030,7 +962,6 @@ __global__ void __launch_bounds__(W * 32, 16 / W) down_kernel(const ExpertParams
       while (left > 0) {
         const uint32_t run = min(Gi - g, left), s0 = pl.seg_s[seg], tokens = m;
         float acc[2][2][4] = {};                                       // [MMA tile][16-row tile]
-        const float none1[1][2] = {}, none2[2][2] = {};
         Weights w;
         auto next = [&]() {
           cp_wait<RING - 1>();
@@ -1050,7 +981,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) down_kernel(const ExpertParams
         } else if (tokens <= 4) {
           auto one = [&](int t) {
             next();
-            unit_products<false, 1>(w, reinterpret_cast<const uint4 (&)[1][4]>(hv[t]), none1, reinterpret_cast<float (&)[1][2][4]>(acc[0]));
+            unit_products<1>(w, reinterpret_cast<const uint4 (&)[1][4]>(hv[t]), reinterpret_cast<float (&)[1][2][4]>(acc[0]));
             fill();
           };
           for (uint32_t k = 0; k < run; k += 2) {
@@ -1064,7 +995,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) down_kernel(const ExpertParams
         } else {
           for (uint32_t k = 0; k < run; ++k) {
             next();
-            unit_products<false, 2>(w, hv, none2, acc);
+            unit_products<2>(w, hv, acc);
             if (k + 1 < run) {
               load_h(hv[0], 0, g + k + 1);
               load_h(hv[1], 1, g + k + 1);

@@ -210,6 +210,23 @@ __device__ __forceinline__ void word_to_frag(uint32_t w, uint32_t (&a)[4]) {
   a[2] = nibbles_to_bf16x2(shr32(w, 8));
   a[3] = nibbles_to_bf16x2(shr32(w, 12));
 }
+// The same as (u - 8) / 4.  Nibble 0 of a half word becomes 128 + u through the exponent
+// bits; nibble 1, in place, is the BF16 subnormal (or smallest normal) 16 u 2^-133, which
+// 2^127 makes u / 4: one shift per word instead of three, and nothing to take off the
+// products.  Both fused operations are exact.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ void word_to_quarters(uint32_t w, uint32_t (&a)[4]) {
+  constexpr uint32_t kQuarter = 0x3E803E80u, kNeg34 = 0xC208C208u, k2p127 = 0x7F007F00u, kNeg2 = 0xC000C000u;
+  const uint32_t w8 = shr32(w, 8);
+  a[0] = fma_bf16x2(nibbles_to_bf16x2(w), kQuarter, kNeg34);
+  a[1] = fma_bf16x2(w & 0x00F000F0u, k2p127, kNeg2);
+  a[2] = fma_bf16x2(nibbles_to_bf16x2(w8), kQuarter, kNeg34);
+  a[3] = fma_bf16x2(w8 & 0x00F000F0u, k2p127, kNeg2);
+}
 __device__ __forceinline__ uint32_t bf16x2_sub136(uint32_t v) {
   const __nv_bfloat162 bias = __floats2bfloat162_rn(136.0f, 136.0f);
   __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&v);

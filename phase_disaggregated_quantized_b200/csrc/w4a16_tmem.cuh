@@ -84,25 +84,6 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The eight nibbles u of a packed word as BF16 (u - 8) / 4, in the order that
-// tcgen05.st.16x256b wants (rows g, g, g + 8, g + 8).  Nibble 0 of a half word becomes
-// 128 + u through the exponent bits; nibble 1, in place, is the BF16 subnormal (or smallest
-// normal) 16 u 2^-133, which 2^127 makes u / 4: a shift less than one of its own.  Both
-// products and sums are exact.
-__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ void quarter_values(uint32_t w, uint32_t* a) {
-  constexpr uint32_t kQuarter = 0x3E803E80u, kNeg34 = 0xC208C208u, k2p127 = 0x7F007F00u, kNeg2 = 0xC000C000u;
-  const uint32_t w8 = w4a16::shr32(w, 8);
-  a[0] = fma_bf16x2(w4a16::nibbles_to_bf16x2(w), kQuarter, kNeg34);     // nibbles 0: row g, first k pair
-  a[2] = fma_bf16x2(w & 0x00F000F0u, k2p127, kNeg2);                     // 1: row g + 8
-  a[1] = fma_bf16x2(w4a16::nibbles_to_bf16x2(w8), kQuarter, kNeg34);    // 2: row g, second k pair
-  a[3] = fma_bf16x2(w8 & 0x00F000F0u, k2p127, kNeg2);                    // 3: row g + 8
-}
-
 template <int NB>
 __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
   using C = Cfg<NB>;
@@ -314,7 +295,12 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint4 v = w[j >> 1];
-              quarter_values(tt ? ((j & 1) ? v.w : v.y) : ((j & 1) ? v.z : v.x), a + 4 * j);
+              uint32_t f[4];                                              // rows g, g + 8, g, g + 8
+              w4a16::word_to_quarters(tt ? ((j & 1) ? v.w : v.y) : ((j & 1) ? v.z : v.x), f);
+              a[4 * j] = f[0];
+              a[4 * j + 1] = f[2];
+              a[4 * j + 2] = f[1];
+              a[4 * j + 3] = f[3];
             }
             tc_st_16x256b_x4(tmem + lanes + ((16u * tt) << 16) + A_COLS * set + 32 * h, a);
           }

@@ -149,7 +149,7 @@ def layer(E, H, I):
     (32, 40, 128, 384, 8), (33, 8, 256, 128, 2), (70, 3, 640, 256, 2), (32, 512, 128, 128, 3),
     # more weights than two units per warp of small CTAs: sixteen warps, every way of cutting the down phase
     (1, 8, 4096, 512, 4), (3, 24, 640, 1408, 8), (32, 24, 896, 640, 4), (20, 48, 384, 1536, 16), (40, 6, 2048, 768, 2), (32, 4, 4096, 1280, 2),
-    # rows of x too long for the table of column offsets
+    # very long rows of x
     (1, 1, 65664, 128, 1), (5, 2, 65664, 128, 1)])
 def test_experts_match_the_oracle(T, E, H, I, topk):
     lay = layer(E, H, I)
