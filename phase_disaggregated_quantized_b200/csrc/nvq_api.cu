@@ -189,27 +189,27 @@ nvq_status launch_dependent(const char* where, void (*kernel)(P...), int grid, i
 }
 
 // More than 8 rows with an epilogue: how many CTAs of a cluster share a 128-row tile's
-// k-groups.  As many as make the longest CTA's work least: rounds over the clusters that a
-// B200 holds at once with one CTA per SM (148 CTAs, 74 clusters of 2, 33 of 4, 15 of 8),
-// each of a slice of the groups (0.3 to 0.4 us per group) and the end of a tile (kEnd, in
-// half groups: fitted to M 16 and 32, N and K from 64 to 24576).  32 rows, one to eight
-// CTAs: N K 64 8192: 26.5, 15.7, 10.7, 7.9 us; 1024 1024: 6.7, 6.4, 6.5, 7.8; 4096 4096:
-// 16.5, 11.6, 9.5, 20.0; 24576 4096: 33.1, 34.1, 47.0, 84.6.
+// k-groups, and how many whole tiles each CTA has before.  What makes the longest CTA's
+// work least: rounds over the clusters that a B200 holds at once with one CTA per SM (148
+// CTAs, 74 clusters of 2, 33 of 4, 15 of 8), each of a slice of the groups (0.3 to 0.4 us
+// per group) and the end of a tile (kEnd, in half groups: fitted to M 16 and 32, N and K
+// from 64 to 24576).  32 rows, one to eight CTAs throughout: N K 64 8192: 26.5, 15.7,
+// 10.7, 7.9 us; 1024 1024: 6.7, 6.4, 6.5, 7.8; 4096 4096: 16.5, 11.6, 9.5, 20.0; 24576
+// 4096: 33.1, 34.1, 47.0, 84.6, and 28.5 with 148 whole tiles, then 44 by two CTAs each.
 struct TmemSplit {
-  uint32_t slog;
-  uint64_t rounds, clusters;
+  uint32_t slog, solo;
+  uint64_t clusters, cost;
 };
 TmemSplit w4a16_tmem_split(int64_t M, int64_t N, int64_t K, int64_t rows) {
   constexpr uint64_t kAtOnce[4] = {148, 74, 33, 15}, kEnd[4] = {6, 15, 18, 24};
   const uint64_t tiles = (uint64_t)((N + 127) / 128) * (uint64_t)((M + rows - 1) / rows), G = (uint64_t)K / 128;
-  TmemSplit best = {};
-  uint64_t least = ~0ull;
+  TmemSplit best = {0, 0, 0, ~0ull};
   for (uint32_t l = 0; l < 4 && (1ull << l) <= G; ++l) {
-    const uint64_t rounds = (tiles + kAtOnce[l] - 1) / kAtOnce[l], cost = rounds * (2 * ((G + (1ull << l) - 1) >> l) + kEnd[l]);
-    if (cost < least) {
-      least = cost;
-      best = {l, rounds, (tiles + rounds - 1) / rounds};
-    }
+    const uint64_t one = 2 * G + kEnd[0], shared = 2 * ((G + (1ull << l) - 1) >> l) + kEnd[l], ctas = kAtOnce[l] << l;
+    const uint64_t rounds = (tiles + kAtOnce[l] - 1) / kAtOnce[l];
+    if (rounds * shared < best.cost) best = {l, 0, (tiles + rounds - 1) / rounds, rounds * shared};
+    const uint64_t solo = l ? tiles / ctas : 0, rest = (tiles - solo * ctas + kAtOnce[l] - 1) / kAtOnce[l];
+    if (solo && solo * one + rest * shared < best.cost) best = {l, (uint32_t)solo, kAtOnce[l], solo * one + rest * shared};
   }
   return best;
 }
@@ -222,6 +222,7 @@ nvq_status launch_w4a16_tmem(nvq::w4a16_tmem::Params p, TmemSplit split, cudaStr
   if (st != NVQ_OK) return st;
   p.slog = split.slog;
   p.slices = 1u << split.slog;
+  p.solo = split.solo;
   return launch_dependent("w4a16_gemm_epilogue", gemm_kernel<NB>, (int)(split.clusters * p.slices), THREADS, Cfg<NB>::SMEM,
                           (int)p.slices, stream, p);
 }
@@ -782,10 +783,6 @@ nvq_status w4a16_gemm_epilogue(const void* x_bf16, const uint8_t* packed_codes, 
     return fail(NVQ_ERR_INVALID_ARG, "w4a16_gemm_epilogue: x overlaps y");
   if (M <= 8) return launch_w4a16<1, false, true>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream, ep);
   const TmemSplit split = w4a16_tmem_split(M, N, K, M <= 16 ? 16 : 32);
-  // Up to 16 rows, where the tiles fill less than 4/5 of their rounds over the SMs, the
-  // streaming kernel, which cuts finer, is faster.
-  if (M <= 16 && split.rounds > 1 && split.clusters * 5 < (148ull >> split.slog) * 4)
-    return launch_w4a16<2, false, true>(x_bf16, packed_codes, packed_scales, y_bf16, M, N, K, stream, ep);
   nvq::w4a16_tmem::Params p = {};
   p.x = static_cast<const __nv_bfloat16*>(x_bf16);
   p.codes = packed_codes;

@@ -22,17 +22,18 @@
 // `full` (a set's four warps stored) and `done` (its MMAs are complete) are the only
 // hand-offs: a set stores group i after `done` of group i - 4, so when group i is full
 // the operands of group i - 4 are free, and the sums of group i - 8 have been read.
-// A tile's k-groups are cut over the CTAs of a cluster, their sums meet in shared memory
-// across it and each CTA finishes a share of the rows; sums are added in a fixed order.
+// A CTA has whole tiles of its own first, where there are enough, then the CTAs of a
+// cluster cut the k-groups of a tile, their sums meet in shared memory across it and each
+// CTA finishes a share of the rows; sums are added in a fixed order.  A tile is finished
+// with the next one's first group under way.
 //
-// Measured (32 rows; the streaming kernel in brackets): N K 4096 12288: 16.2 us (26.1),
-// 4096 4096: 9.5 (15.5), 1024 8192: 9.9 (15.2), 16384 4096: 18.2 (29.5), 24576 4096: 33.1
-// (40.2); 16 rows: 13.0 (15.0), 7.8 (8.6), -, 18944 4096: 15.3 (19.4).  An MMA takes 45
+// Measured (32 rows; the streaming kernel in brackets): N K 4096 12288: 16.1 us (26.1),
+// 4096 4096: 9.7 (15.5), 1024 8192: 10.0 (15.2), 16384 4096: 18.1 (29.5), 24576 4096: 28.5
+// (40.2); 16 rows: 13.3 (15.0), 8.0 (8.6), 8.0 (8.3), -, 23.1 (23.9).  An MMA takes 45
 // cycles issued alone, whatever N up to 64, 75 to 100 here; a group 560 cycles for 16 rows
 // and 740 for 32, in which the ALUs (80 instructions per unit for the nibbles) are half
 // busy.  With two sets and one MMA warp a group took 1700 cycles: that warp's waits and
-// commits are not free.  What is left is the chain MMAs -> `done` -> dequantize -> `full`
-// and, for large N, rounds of tiles that do not fill the SMs.
+// commits are not free.  What is left is the chain MMAs -> `done` -> dequantize -> `full`.
 #pragma once
 #include <cuda_bf16.h>
 #include "epilogue.cuh"
@@ -74,6 +75,7 @@ struct Params {
   const uint8_t* scales;
   __nv_bfloat16* y;
   uint32_t M, N, K, slices, slog;             // slices = 2^slog CTAs of a cluster
+  uint32_t solo;                              // rounds in which each CTA has a tile of its own, before those that the cluster shares
   EpiParams ep;
 };
 
@@ -94,23 +96,29 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
   const uint32_t full = sbase + C::OFF_BAR, done = full + 8 * STAGES, drain_bar = done + 8 * STAGES;
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + C::OFF_BAR + 8 * C::NUM_BARS);
   const uint32_t G = p.K >> 7, rank = w4a16::cluster_rank(), cid = w4a16::cluster_id(), nclu = w4a16::cluster_count();
-  const uint32_t k0 = (uint32_t)((uint64_t)G * rank >> p.slog), nk = (uint32_t)((uint64_t)G * (rank + 1) >> p.slog) - k0;   // >= 1
   const uint32_t ntile = (p.N + ROWS - 1) / ROWS, tiles = ntile * ((p.M + NB - 1) / NB), utiles = p.N >> 5;
+  // This CTA's jobs: `solo` whole tiles, then its share of the k-groups of its cluster's tiles.
+  const uint32_t first_shared = p.solo * (nclu << p.slog) + cid;
+  const uint32_t jobs = p.solo + (first_shared < tiles ? (tiles - 1 - first_shared) / nclu + 1 : 0u);
+  const uint32_t share0 = (uint32_t)((uint64_t)G * rank >> p.slog), share = (uint32_t)((uint64_t)G * (rank + 1) >> p.slog) - share0;   // >= 1
+  auto tile_of = [&](uint32_t j) { return j < p.solo ? (j * nclu + cid) * p.slices + rank : first_shared + (j - p.solo) * nclu; };
+  auto k0_of = [&](uint32_t j) { return j < p.solo ? 0u : share0; };
+  auto nk_of = [&](uint32_t j) { return j < p.solo ? G : share; };
 
   // ---- dequantizing warps: the units of this warp, in the order of its groups
   const uint32_t q = warp & 3u, set = warp >> 2;
   const uint32_t ring = sbase + C::OFF_RING + warp * RING * SLOT;
-  uint32_t rtile = cid, rk = set, rslot = ring + 16 * lane, rn = 0;
+  uint32_t rjob = 0, rk = set, rnk = 0, rslot = ring + 16 * lane, rn = 0;
   const uint8_t *rcodes = nullptr, *rscales = nullptr;
   bool rvalid = false;
-  auto locate = [&]() {                       // from group rk of tile rtile on, which may lie past the tile's end
-    while (rk >= nk) {
-      rk -= nk;
-      rtile += nclu;
+  auto locate = [&]() {                       // from group rk of job rjob on, which may lie past the job's end
+    while (rk >= (rnk = nk_of(rjob))) {
+      rk -= rnk;
+      ++rjob;
     }
-    const uint32_t u = 4 * (rtile % ntile) + q;
-    rvalid = rtile < tiles && u < utiles;
-    const size_t unit = (size_t)u * G + k0 + rk;
+    const uint32_t u = 4 * (tile_of(rjob) % ntile) + q;
+    rvalid = rjob < jobs && u < utiles;
+    const size_t unit = (size_t)u * G + k0_of(rjob) + rk;
     rcodes = p.codes + unit * 2048 + 16 * lane;
     rscales = p.scales + unit * 64 + 16 * lane;
   };
@@ -128,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
     }
     rcodes += STAGES * 2048;
     rscales += STAGES * 64;
-    if ((rk += STAGES) >= nk) locate();
+    if ((rk += STAGES) >= rnk) locate();
   };
   if (warp < DWARPS) {                        // constant inputs: requested while the kernel before ends
     locate();
@@ -162,12 +170,12 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
     const uint32_t row = q * 32 + lane, lanes = (q * 32u) << 16;
     // bf16 scales of row r of a unit at 4 (r % 8) + 2 (r / 16) + (r / 8) % 2.
     const uint32_t s_at = 2048 + 2 * (4 * (lane & 7u) + 2 * (lane >> 4) + ((lane >> 3) & 1u));
-    float acc[NB];                                                        // a quarter of the sums of tile `summed`
+    float acc[NB];                                                        // a quarter of the sums of job `summed`
 #pragma unroll
     for (int t = 0; t < NB; ++t) acc[t] = 0.f;
-    uint32_t summed = cid;
-    auto has_rows = [&](uint32_t tile) { return 4 * (tile % ntile) + q < utiles; };
-    bool sum_valid = has_rows(cid);
+    uint32_t summed = 0;
+    auto has_rows = [&](uint32_t job) { return 4 * (tile_of(job) % ntile) + q < utiles; };
+    bool sum_valid = has_rows(0);
     auto wait_done = [&](uint32_t i) {
       if (ok) ok = warp_mbar_wait(done + 8 * set, (i / STAGES) & 1u);
     };
@@ -183,14 +191,16 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
         for (int t = 0; t < 16; ++t) acc[t0 + t] = __fmaf_rn(scale, __uint_as_float(v[t]), acc[t0 + t]);
       }
     };
-    // Finishes tile `summed`: every warp's sums, then four rows of one token for each of this thread's outputs.
+    // Finishes job `summed`: every warp's sums, then four rows of one token for each of this thread's outputs.
     auto finish = [&]() {
-      const uint32_t mb = summed / ntile, nt = summed - mb * ntile;
-      const uint32_t rows = ROWS >> p.slog, qlog = 5 - p.slog, items = NB << qlog;
+      const bool shared = p.slices > 1 && summed >= p.solo;
+      const uint32_t tile = tile_of(summed), mb = tile / ntile, nt = tile - mb * ntile;
+      const uint32_t parts = shared ? p.slices : 1u, from = shared ? 0u : rank;   // the CTAs whose sums these are
+      const uint32_t slog = shared ? p.slog : 0u, qlog = 5 - slog, items = NB << qlog, row0 = shared ? rank * (ROWS >> slog) : 0u;
       constexpr int ITEMS = NB * 32 / DTHREADS;
       auto output = [&](uint32_t it, uint32_t& t, uint32_t& r, uint32_t& m, uint32_t& n) {
         t = it >> qlog;
-        r = rank * rows + 4 * (it & ((1u << qlog) - 1));
+        r = row0 + 4 * (it & ((1u << qlog) - 1));
         m = mb * NB + t;
         n = nt * ROWS + r;
         return it < items && m < p.M && n < p.N;
@@ -202,7 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
         for (int j = 0; j < ITEMS; ++j)
           if (output(threadIdx.x + j * DTHREADS, t, r, m, n))
             res[j] = *reinterpret_cast<const uint2*>(p.ep.residual + (size_t)m * p.ep.ldr + n);
-      if (p.slices > 1 && summed != cid) {
+      if (shared && summed > p.solo) {
         __syncwarp();
         w4a16::cluster_wait();                                            // the other CTAs have read the last tile's sums
       }
@@ -214,7 +224,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
       if (set < 2)
 #pragma unroll
         for (int j = 0; j < NB; ++j) mine[j * PSTRIDE] += acc[j];
-      if (p.slices > 1) {
+      if (shared) {
         __syncwarp();
         w4a16::cluster_arrive();
         w4a16::cluster_wait();
@@ -228,10 +238,10 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
           const uint32_t at = sbase + C::OFF_PART + (t * PSTRIDE + r) * 4;
           float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-          for (uint32_t k = 0; k < p.slices; ++k) {
+          for (uint32_t k = 0; k < parts; ++k) {
             float4 f[2];
 #pragma unroll
-            for (uint32_t z = 0; z < 2; ++z) f[z] = w4a16::ld_cluster_f32x4(at + z * NB * PSTRIDE * 4, k, after);
+            for (uint32_t z = 0; z < 2; ++z) f[z] = w4a16::ld_cluster_f32x4(at + z * NB * PSTRIDE * 4, from + k, after);
 #pragma unroll
             for (uint32_t z = 0; z < 2; ++z) {
               v[0] += f[z].x; v[1] += f[z].y; v[2] += f[z].z; v[3] += f[z].w;
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
           }
           *reinterpret_cast<uint2*>(p.y + (size_t)m * p.ep.ldy + n) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
         }
-      if (p.slices > 1) {
+      if (shared) {
         __syncwarp();
         w4a16::cluster_arrive();
       } else {
@@ -257,22 +267,21 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
       }
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[j] = 0.f;
-      summed += nclu;
-      sum_valid = has_rows(summed);
+      sum_valid = has_rows(++summed);
     };
 
     float before = 0.f;                                                   // scale of this set's group before, whose sums are still in TMEM
-    uint32_t i = set, k = set, tile = cid;                                // this set's next group: k of `tile`
+    uint32_t i = set, k = set, job = 0, nk = nk_of(0);                    // this set's next group: k of `job`
     bool valid = sum_valid;
     for (;; i += STAGES, k += STAGES) {
       if (k >= nk) {
         while (k >= nk) {
           k -= nk;
-          tile += nclu;
+          nk = nk_of(++job);
         }
-        valid = has_rows(tile);
+        valid = has_rows(job);
       }
-      if (tile >= tiles) break;
+      if (job >= jobs) break;
       cp_wait<RING - 1>();
       __syncwarp();                                                       // the scales came through other lanes
       float scale = 0.f;
@@ -314,14 +323,14 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
       slot = slot == ring + (RING - 1) * SLOT ? ring : slot + SLOT;
       if (i >= STAGES) drain(i - STAGES, before);
       before = scale;
-      while (summed != tile) finish();                                    // with the next tile's first group under way
+      while (summed != job) finish();                                     // with the next job's first group under way
     }
     if (i >= STAGES) {                                                    // the last group of this set
       wait_done(i - STAGES);
       drain(i - STAGES, before);
     }
-    while (summed < tiles) finish();
-    if (p.slices > 1) w4a16::cluster_wait();                              // nobody reads this CTA's sums any more
+    while (summed < jobs) finish();
+    if (p.slices > 1 && jobs > p.solo) w4a16::cluster_wait();                              // nobody reads this CTA's sums any more
   } else {
     // Stage st: X of groups st, st + 4, ... and their MMAs.  A lane loads k 8 u .. 8 u + 7 of
     // rows 2 r + half, a group of its own ahead; k = 32 c + 4 j + e is column 16 j + 4 c + e
@@ -332,19 +341,24 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
     const uint64_t bdesc = smem_desc(sbase + 2 * st * C::XSTAGE, 0, 1024, kSwizzle128B);
     const uint32_t row_bytes = 2 * p.K;                                  // 32 rows of them fit in 32 bits
     uint4 v[NB / 2] = {};
-    uint32_t xtile = cid, xk = st;                                        // the next group loaded
+    const uint32_t groups = p.solo * G + (jobs - p.solo) * share;
+    uint32_t xi = st, xjob = 0, xend = 0, xlast = 0;                      // the next group loaded, its job and that job's end
+    const uint8_t* xfrom = nullptr;
     auto load = [&]() {
-      while (xk >= nk) {
-        xk -= nk;
-        xtile += nclu;
+      if (xi >= groups) return;
+      if (xi >= xend) {                                                   // the first one of another job
+        uint32_t begin = xend;
+        for (; xi >= (xend = begin + nk_of(xjob)); ++xjob) begin = xend;
+        const uint32_t m0 = tile_of(xjob) / ntile * NB;
+        xlast = min((uint32_t)NB, p.M - m0) - 1;
+        xfrom = reinterpret_cast<const uint8_t*>(p.x + (size_t)m0 * p.K + (size_t)k0_of(xjob) * 128) + 16 * u - (size_t)begin * 256;
+        ++xjob;
       }
-      if (xtile >= tiles) return;
-      const uint32_t m0 = xtile / ntile * NB, last = min((uint32_t)NB, p.M - m0) - 1;
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(p.x + (size_t)m0 * p.K + (size_t)(k0 + xk) * 128) + 16 * u;
+      const uint8_t* src = xfrom + (size_t)xi * 256;
 #pragma unroll
       for (uint32_t r = 0; r < NB / 2; ++r)                               // past M: the last row again, for sums that are dropped
-        v[r] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)min(2 * r + half, last) * row_bytes));
-      xk += STAGES;
+        v[r] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)min(2 * r + half, xlast) * row_bytes));
+      xi += STAGES;
     };
     auto store = [&](uint32_t buf) {
 #pragma unroll
@@ -359,8 +373,9 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
     load();
     store(0);
     load();
-    uint32_t i = st, end = nk, buf = 0;
-    for (uint32_t tile = cid; tile < tiles; tile += nclu, end += nk) {
+    uint32_t i = st, end = 0, buf = 0;
+    for (uint32_t job = 0; job < jobs; ++job) {
+      end += nk_of(job);
 #pragma unroll 1
       for (; i < end; i += STAGES, buf ^= 1u) {
         if (lane == 0) {
@@ -380,8 +395,8 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
         store(buf ^ 1u);
         load();
       }
-      if (p.slices > 1) {                                                 // this warp's part in the cluster's barriers, a tile behind
-        if (tile != cid) {
+      if (p.slices > 1 && job >= p.solo) {                                // this warp's part in the cluster's barriers, a job behind
+        if (job > p.solo) {
           w4a16::cluster_wait();
           w4a16::cluster_arrive();
           w4a16::cluster_wait();
@@ -389,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
         w4a16::cluster_arrive();
       }
     }
-    if (p.slices > 1) {
+    if (p.slices > 1 && jobs > p.solo) {
       w4a16::cluster_wait();
       w4a16::cluster_arrive();
       w4a16::cluster_wait();

@@ -86,3 +86,44 @@ def test_binding_refuses_host_tensors():
         nvq.nvfp4_gemm_w4a4_epilogue((x, x, x), (x, x, x), 2, 32, 128)
     with pytest.raises(ValueError, match="CUDA"):
         nvq.nvq_linear_epilogue(x, N=32)
+
+
+# ------------------------------------------------------------------ the work split of the INT4 product with more than 8 rows
+def tmem_split(tiles, G):
+    """(log2 of the CTAs per cluster, rounds of whole tiles, clusters), as the host chooses them."""
+    at_once, end, best, least = (148, 74, 33, 15), (6, 15, 18, 24), None, 1 << 62
+    for l in range(4):
+        if (1 << l) > G:
+            break
+        one, shared, ctas = 2 * G + end[0], 2 * -(-G // (1 << l)) + end[l], at_once[l] << l
+        rounds = -(-tiles // at_once[l])
+        if rounds * shared < least:
+            best, least = (l, 0, -(-tiles // rounds)), rounds * shared
+        solo = tiles // ctas if l else 0
+        cost = solo * one + -(-(tiles - solo * ctas) // at_once[l]) * shared
+        if solo and cost < least:
+            best, least = (l, solo, at_once[l]), cost
+    return best
+
+
+@pytest.mark.parametrize("tiles", [1, 2, 15, 16, 33, 34, 74, 75, 99, 148, 149, 150, 192, 223, 296, 297, 700])
+@pytest.mark.parametrize("G", [1, 2, 3, 7, 8, 32, 48, 128, 400])
+def test_int4_jobs_cover_every_tile_and_group_once(tiles, G):
+    slog, solo, clusters = tmem_split(tiles, G)
+    slices = 1 << slog
+    seen = {}
+    for cid in range(clusters):
+        first = solo * (clusters << slog) + cid
+        jobs = solo + ((tiles - 1 - first) // clusters + 1 if first < tiles else 0)
+        assert jobs >= 1
+        for rank in range(slices):
+            for j in range(jobs):
+                whole = j < solo
+                tile = (j * clusters + cid) * slices + rank if whole else first + (j - solo) * clusters
+                k0, k1 = (0, G) if whole else (G * rank >> slog, G * (rank + 1) >> slog)
+                assert 0 <= tile < tiles and k0 < k1
+                seen.setdefault(tile, []).append((k0, k1))
+    assert sorted(seen) == list(range(tiles))
+    for parts in seen.values():
+        parts.sort()
+        assert parts[0][0] == 0 and parts[-1][1] == G and all(a[1] == b[0] for a, b in zip(parts, parts[1:]))

@@ -84,8 +84,10 @@ def _cu(t):
 
 INT4_SHAPES = [(1, 32, 128), (1, 4096, 256), (7, 96, 384), (8, 2080, 1152), (9, 64, 128), (16, 352, 4096),
                (17, 32, 256), (32, 1056, 384), (33, 96, 128), (70, 64, 640),
-               # more than 8 rows: k-groups cut over 8, 4 or 2 CTAs, several rounds of tiles, tiles of one group
-               (12, 64, 8192), (20, 96, 1152), (13, 2080, 2048), (25, 8224, 1024), (16, 18976, 128), (24, 19104, 640), (320, 1920, 6144)]
+               # more than 8 rows: k-groups cut over 8, 4 or 2 CTAs, several rounds of tiles, tiles of one group,
+               # whole tiles and then shared ones, several rounds of shared ones
+               (12, 64, 8192), (20, 96, 1152), (13, 2080, 2048), (25, 8224, 1024), (16, 18976, 128), (24, 19104, 640),
+               (320, 1920, 2048), (320, 1920, 6144), (320, 1024, 16384), (896, 1024, 16384)]
 NVFP4_SHAPES = [(1, 8, 64), (5, 264, 128), (31, 72, 192), (128, 256, 256), (129, 520, 1088), (300, 1000, 320),
                 (1030, 2312, 64),
                 # few tiles, whose k-stages 8, 4 or 2 CTAs split
