@@ -267,7 +267,12 @@ typedef struct {
   int activation; /* an nvq_activation */
 } nvq_epilogue;
 
-/* nvfp4_gemm_w4a4 with an epilogue: arguments and shape rules as there. */
+/* nvfp4_gemm_w4a4 with an epilogue: arguments and shape rules as there.
+ * Launched with programmatic dependent launch: the call may begin while the
+ * preceding kernel on the stream is still finishing, but before it has waited
+ * for that kernel it only prefetches weights into L2.  It lets the next kernel
+ * launch early in turn, under the rule of w4a16_gemm: one launched that way must
+ * execute griddepcontrol.wait before it reads y. */
 nvq_status nvfp4_gemm_w4a4_epilogue(const uint8_t* x_codes, const uint8_t* x_scales, const float* t_x,
                                     const uint8_t* w_codes, const uint8_t* w_scales, const float* t_w,
                                     void* y_bf16, int64_t M, int64_t N, int64_t K,
@@ -456,11 +461,11 @@ nvq_status nvq_linear_epilogue(const void* x_bf16, int64_t M, int64_t N, int64_t
  * workspace: w4a16_moe_workspace_bytes(T, H, I, topk) device bytes, 16-byte
  * aligned, of any content; calls that may overlap on the GPU need one each.
  * Launched with programmatic dependent launch under the rules of w4a16_gemm
- * (packed weights constant, all else after the wait on the preceding kernel).
+ * (packed and router weights constant, all else after the wait on the preceding
+ * kernel).
  * Shape rules: T >= 0, 1 <= E <= 512, 1 <= topk <= 16; router: topk <= E,
  * H % 64 == 0; experts: H % 128 == 0, I % 128 == 0, both < 2^20, H * I < 2^33.
- * Pointers
- * 16-byte aligned, ids and weights 4.
+ * Pointers 16-byte aligned, ids and weights 4.
  * ------------------------------------------------------------------------ */
 nvq_status moe_route(const void* x_bf16, const void* w_router_bf16, int64_t T, int64_t E, int64_t H, int topk,
                      int renormalize, int32_t* ids, float* weights, void* stream);

@@ -201,7 +201,7 @@ route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restric
     for (uint32_t i = threadIdx.x; i < nt * row4; i += RTHREADS) {
       const uint32_t t = i / row4, w = i - t * row4;
       *reinterpret_cast<uint4*>(xs + t * RXROW + w * 16) =
-          __ldg(reinterpret_cast<const uint4*>(x + (size_t)(t0 + t) * H + (size_t)c0 * 64) + w);
+          reinterpret_cast<const uint4*>(x + (size_t)(t0 + t) * H + (size_t)c0 * 64)[w];
     }
     __syncthreads();
     float acc[NTK][4] = {};
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(W * 32, 16 / W) gate_up_kernel(const ExpertPar
     };
     auto load_x = [&](const uint4* row, uint32_t at, uint4 (&b)[4]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = __ldg(row + at * 16 + i);
+      for (int i = 0; i < 4; ++i) b[i] = row[at * 16 + i];
     };
     if (any) {
       const uint4* row = row_of(seg);

@@ -449,7 +449,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
     const uint32_t q = warp & 3u;                             // TMEM sub-partition of this warp
     const uint32_t h = (warp - 2) >> 2;                       // which 64-column chunk of each pair
     const uint32_t row = q * 32 + lane;                       // row of the tile held by this thread
-    const float alpha = __ldg(p.t_x) * __ldg(p.t_w);
+    const float alpha = __ldcg(p.t_x) * __ldcg(p.t_w);      // the kernel before may have written them
     if constexpr (EPI == 0) {
     uint8_t* cbuf = smem + OFF_C + (warp - 2) * C_BYTES;      // this warp's 32 x 128 B staging
     const uint32_t cbuf_s = smem_addr(cbuf);
@@ -601,7 +601,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * e + i]) * alpha;
           if (p.epi.bias != nullptr && col0 + 8 * e < p.N) {   // N % 8 == 0
-            const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.epi.bias + col0 + 8 * e));
+            const uint4 b = *reinterpret_cast<const uint4*>(p.epi.bias + col0 + 8 * e);
             f[0] += bf16_lo(b.x); f[1] += bf16_hi(b.x); f[2] += bf16_lo(b.y); f[3] += bf16_hi(b.y);
             f[4] += bf16_lo(b.z); f[5] += bf16_hi(b.z); f[6] += bf16_lo(b.w); f[7] += bf16_hi(b.w);
           }

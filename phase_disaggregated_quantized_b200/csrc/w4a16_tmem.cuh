@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
       const uint8_t* src = xfrom + (size_t)xi * 256;
 #pragma unroll
       for (uint32_t r = 0; r < NB / 2; ++r)                               // past M: the last row again, for sums that are dropped
-        v[r] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)min(2 * r + half, xlast) * row_bytes));
+        v[r] = __ldcg(reinterpret_cast<const uint4*>(src + (size_t)min(2 * r + half, xlast) * row_bytes));
       xi += STAGES;
     };
     auto store = [&](uint32_t buf) {
