@@ -12,7 +12,10 @@ Prefill (Mix-Quant page, gist.science, section 2): ``nvfp4_quantize`` then
 ``int4_pack_weights`` offline, then ``w4a16_gemm``.  ``nvq_linear`` picks one
 of the two by the batch size M (Disaggregated Quantization page,
 singularity-lens.com: one master weight kept in both formats).  The calls
-ending in ``_epilogue`` add bias, activation and residual to those products.
+ending in ``_epilogue`` add bias, activation and residual to those products;
+``moe_route``, ``w4a16_moe_experts`` and ``w4a16_moe`` are the mixture-of-experts
+layer of a few tokens.  These calls go through a small compiled module
+(``_binding.so``), the others through ctypes.
 """
 from __future__ import annotations
 
