@@ -8,9 +8,9 @@
 //
 // Three launches chained by programmatic dependent launch: the router, gate and
 // up, down.  (One cooperative launch with grid barriers between the phases was
-// slower for few tokens, 12.3 against 9.4 us for 1344 units of weights, and equal
-// for the largest batches, 217 and 219 us for 360448: a grid barrier takes 1.8 us and
-// the gap before a cooperative launch 2.6, a dependent launch 0.75.)  The experts are in the packed
+// slower for few tokens, 12.3 against 9.9 us for 1344 units of weights, and equal
+// for the largest batches: a grid barrier takes 1.8 us and the gap before a cooperative
+// launch 2.6, a dependent launch 0.75.)  The experts are in the packed
 // form of the decode GEMM (units of 32 rows x 128 k), gate and up rows in turn by
 // 16, so that one unit holds 16 gate rows (MMA tile 0) and the matching 16 up rows
 // (tile 1) and a lane has both halves of its h.  Weights are read from memory once
@@ -628,8 +628,8 @@ struct Smem {
 // slower, whole tiles, or even parts of the flat sequence of units.  With 8 warps a
 // round (one unit per warp) takes about 0.6 us, 0.4 us for one row tile of the unit, and
 // joining cut tiles through memory 2.5 us, which with the rounding down of `joined` is
-// five rounds.  With 16 warps a round takes longer, so four: 21.9 us for 16 experts of
-// 704 units (24.6 with two), 45.0 for 52 of 704 (47.1 with six).
+// five rounds.  With 16 warps a round takes longer, so four: 20.3 us for 16 experts of
+// 704 units (23.3 with two), 43.1 for 52 of 704 (44.6 with six).
 template <int W>
 __device__ __forceinline__ DownCut cut_down(const ExpertParams& p, uint32_t segments, uint32_t ntile, uint32_t Gi) {
   DownCut d;

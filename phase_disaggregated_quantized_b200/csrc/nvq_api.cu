@@ -965,8 +965,8 @@ nvq_status launch_experts(nvq::moe::ExpertParams p, int64_t T, void* workspace, 
     const int64_t units = std::min<int64_t>(p.E, (int64_t)p.T * p.topk) * (p.I / 16) * (p.H / 128);
     // Up to two units of gate and up weights per warp of eight-warp CTAs: both kernels'
     // CTAs fit on an SM, and down has its plan and first weights when h is complete
-    // (512 units: 8.2 us, and 8.9 with 16 warps; 2048: 10.5 and 10.8).  More want all
-    // warps on the weights (4096 units: 13.5 us with 8 warps, 12.2 with 16; 73216: 53 and 45).
+    // (512 units: 7.1 us, and 8.2 with 16 warps; 2048: 9.1 and 10.0).  More want all
+    // warps on the weights (4096 units: 12.1 us with 8 warps, 11.4 with 16; 73216: 49.7 and 43.1).
     const nvq_status st = units <= 2 * 8 * grid ? launch_experts_32<8>(p, grid, stream) : launch_experts_32<16>(p, grid, stream);
     if (st != NVQ_OK) return st;
     p.x += (size_t)p.T * p.H;

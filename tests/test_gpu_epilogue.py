@@ -228,8 +228,9 @@ def test_repeated_and_concurrent_calls_agree():
         assert torch.equal(p, ra) and torch.equal(q, rb)
 
 
-def test_captured_and_replayed_on_new_inputs():
-    x, w, bias, res = _draw(4, 256, 256, seed=6)
+@pytest.mark.parametrize("M", [4, 20, 50])
+def test_captured_and_replayed_on_new_inputs(M):
+    x, w, bias, res = _draw(M, 256, 256, seed=6)
     op = Int4(x, w)
     stream = res.cuda()
     op(bias=bias.cuda(), residual=stream.clone(), activation="gelu")
@@ -241,12 +242,42 @@ def test_captured_and_replayed_on_new_inputs():
         op(bias=bc, residual=stream, y=stream, activation="gelu")
         op(bias=bc, residual=stream, y=stream, activation="gelu")     # reads what the first wrote
     for seed in (7, 8):
-        x2, _, _, res2 = _draw(4, 256, 256, seed=seed)
+        x2, _, _, res2 = _draw(M, 256, 256, seed=seed)
         op.x.copy_(x2)
         stream.copy_(res2)
         g.replay()
         want = op(bias=bc, residual=op(bias=bc, residual=res2.cuda(), activation="gelu"), activation="gelu")
         assert torch.equal(stream, want)
+
+
+@pytest.mark.parametrize("M", [1, 8, 12, 20, 40])
+@pytest.mark.parametrize("form", ["w4a16", "w4a4", "both"])
+def test_calls_that_read_what_the_last_one_wrote(form, M):
+    """Forty calls on two buffers, each reading one and updating the other, launched one after
+    the other while the last one ends: the same bits as with a wait after every call."""
+    N = 512
+    _, w, bias, res = _draw(M, N, N, seed=M)
+    i4 = nvq.int4_pack_weights(*nvq.int4_quantize(w.cuda()), N, N)
+    f4, bc = nvq.nvfp4_quantize(w.cuda()), (0.1 * bias).cuda()
+
+    def chain(wait):
+        a, b = res.cuda(), (0.5 * res).cuda()
+        for k in range(40):
+            if form == "w4a16" or (form == "both" and k % 3 != 2):
+                nvq.w4a16_gemm_epilogue(a, *i4, N, bias=bc, activation="silu", residual=b, y=b)
+            else:
+                nvq.nvfp4_gemm_w4a4_epilogue(nvq.nvfp4_quantize(a), f4, M, N, N, bias=bc, activation="silu", residual=b, y=b)
+            if wait:
+                torch.cuda.synchronize()
+            b = 0.75 * b if k % 5 == 4 else b                # a kernel of another kind in between
+            a, b = b, a
+        return a, b
+
+    want = chain(True)
+    for _ in range(3):
+        got = chain(False)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.isfinite(want[0]).all()
 
 
 @pytest.mark.parametrize("M", [1, 16, 17, 200])
