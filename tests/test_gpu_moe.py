@@ -281,6 +281,32 @@ def test_repeated_and_concurrent_calls_agree():
             assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
+@pytest.mark.parametrize("T, E, H, I, topk", [(1, 40, 128, 384, 8), (3, 24, 640, 1408, 8), (40, 40, 128, 384, 8)])
+def test_layers_that_read_what_the_last_one_wrote(T, E, H, I, topk):
+    """Layer after layer in place, launched one after the other while the last one ends: the
+    same bits as with a wait after every call."""
+    lay = layer(E, H, I)
+    wr = (torch.randn(E, H, generator=torch.Generator().manual_seed(13)) * 0.1).to(torch.bfloat16).cuda()
+
+    def chain(wait):
+        x, seen = synth.activations(T, H, seed=T).cuda(), []
+        for k in range(30):
+            _, ids, w = nvq.w4a16_moe(x, wr, lay.gate_up, lay.down, I, topk, residual=x, y=x)
+            if k % 4 == 1:
+                lay(x, ids, w, residual=x, y=x)              # the experts alone, with the same choices
+            if wait:
+                torch.cuda.synchronize()
+            x = (x.float() / x.float().square().mean(1, keepdim=True).sqrt()).to(torch.bfloat16)   # a layer's output grows with the square of x
+            seen.append(ids)
+        return x, torch.stack(seen)
+
+    want = chain(True)
+    assert torch.isfinite(want[0]).all()
+    for _ in range(3):
+        got = chain(False)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_captured_layer_follows_new_inputs():
     lay = layer(8, 256, 128)
     g = torch.Generator().manual_seed(12)
