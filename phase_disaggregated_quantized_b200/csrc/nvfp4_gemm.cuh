@@ -229,8 +229,8 @@ __device__ __forceinline__ uint32_t acc_col(uint32_t buf) { return buf ? ACC1_CO
 // cluster, in rank order.  There a tile has its SM to itself: a k-stage takes 0.8 to
 // 1.3 us (the loads of one SM), and the epilogue has no next tile to hide behind, so
 // more CTAs per tile shorten both (M 400, N 1000, K 8192: 32.1 us as EPI 2, 14.8 with
-// four CTAs; M 777, N 5128, K 1088: 15.9 and, with one, 14.2; M 3, N 1208, K 64: 10.1
-// and 6.3, there for the plain stores in place of TMA's).
+// four CTAs; M 777, N 5128, K 1088: 15.9 and, with one, 13.4; M 3, N 1208, K 64: 10.1
+// and 6.4, there for the plain stores in place of TMA's).
 template <int EPI>
 __global__ void __launch_bounds__(THREADS, 1)
 nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -718,13 +718,16 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
   }
   if constexpr (EPI == 3) {
     // Every rank finishes its share of the tile's rows: a warp a row at a time, a lane
-    // columns 4 lane .. and 128 + 4 lane .. of it.
-    w4a16::cluster_arrive();
-    w4a16::cluster_wait();
+    // columns 4 lane .. and 128 + 4 lane .. of it.  The next row's residual, and sums that
+    // are one slice's alone, are requested before a row is computed.
+    const uint32_t slices = gridDim.x / num_tiles, slog = __ffs(slices) - 1, rank = w4a16::cluster_rank();   // a power of two
+    if (slices > 1) {
+      w4a16::cluster_arrive();
+      w4a16::cluster_wait();
+    }
     const uint32_t after = w4a16::after_cluster_wait();
     uint32_t mt, nt;
     tile_coords(first_tile, p, mt, nt);
-    const uint32_t slices = gridDim.x / num_tiles, slog = __ffs(slices) - 1, rank = w4a16::cluster_rank();   // a power of two
     const uint32_t rows = min((uint32_t)BM, p.M - mt * BM), r1 = rows * (rank + 1) / slices;
     const uint32_t col = nt * BN + 4 * lane;
     const bool in[2] = {col < p.N, col + 128 < p.N};           // N % 8 == 0
@@ -732,39 +735,62 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       if (p.epi.bias && in[j]) bias[j] = *reinterpret_cast<const uint2*>(p.epi.bias + col + 128 * j);
-#pragma unroll 2
-    for (uint32_t r = rows * rank / slices + warp; r < r1; r += THREADS / 32) {
-      const size_t m = mt * BM + r;
-      uint2 res[2] = {};
-      float v[2][4] = {};
+    const bool alone = slices == 1 || p.num_k_stages == 1;    // only the last rank's slice has a stage
+    auto sums_of = [&](uint32_t r, uint32_t k, float4 (&f)[2]) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) f[j] = w4a16::ld_cluster_f32x4(sbase + (r * PART_STRIDE + 4 * lane + 128 * j) * 4, k, after);
+    };
+    auto residual_of = [&](uint32_t r, uint2 (&q)[2]) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        if (p.epi.residual && in[j]) res[j] = *reinterpret_cast<const uint2*>(p.epi.residual + m * p.epi.ldr + col + 128 * j);
+        if (p.epi.residual && in[j]) q[j] = *reinterpret_cast<const uint2*>(p.epi.residual + (size_t)(mt * BM + r) * p.epi.ldr + col + 128 * j);
+    };
+    float4 f[2] = {};
+    uint2 res[2] = {};
+    uint32_t r = rows * rank / slices + warp;
+    if (r < r1) {
+      residual_of(r, res);
+      if (alone) sums_of(r, slices - 1, f);
+    }
+#pragma unroll 2
+    for (; r < r1; r += THREADS / 32) {
+      float4 fn[2] = {};
+      uint2 rn[2] = {};
+      if (r + THREADS / 32 < r1) {
+        residual_of(r + THREADS / 32, rn);
+        if (alone) sums_of(r + THREADS / 32, slices - 1, fn);
+      }
+      float v[8] = {f[0].x, f[0].y, f[0].z, f[0].w, f[1].x, f[1].y, f[1].z, f[1].w};
+      if (!alone)
 #pragma unroll 4
-      for (uint32_t k = 0; k < slices; ++k) {
-        if ((p.num_k_stages * (k + 1)) >> slog == (p.num_k_stages * k) >> slog) continue;   // a slice without a stage
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {                          // columns past N hold sums of nothing, inside the row
-          const float4 f = w4a16::ld_cluster_f32x4(sbase + (r * PART_STRIDE + 4 * lane + 128 * j) * 4, k, after);
-          v[j][0] += f.x; v[j][1] += f.y; v[j][2] += f.z; v[j][3] += f.w;
+        for (uint32_t k = 0; k < slices; ++k) {
+          if ((p.num_k_stages * (k + 1)) >> slog == (p.num_k_stages * k) >> slog) continue;   // a slice without a stage
+          float4 g[2];                                          // columns past N hold sums of nothing, inside the row
+          sums_of(r, k, g);
+          v[0] += g[0].x; v[1] += g[0].y; v[2] += g[0].z; v[3] += g[0].w;
+          v[4] += g[1].x; v[5] += g[1].y; v[6] += g[1].z; v[7] += g[1].w;
         }
-      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        v[j][0] += bf16_lo(bias[j].x); v[j][1] += bf16_hi(bias[j].x); v[j][2] += bf16_lo(bias[j].y); v[j][3] += bf16_hi(bias[j].y);
+        v[4 * j] += bf16_lo(bias[j].x); v[4 * j + 1] += bf16_hi(bias[j].x);
+        v[4 * j + 2] += bf16_lo(bias[j].y); v[4 * j + 3] += bf16_hi(bias[j].y);
       }
-      float (&flat)[8] = reinterpret_cast<float (&)[8]>(v);
-      activate(flat, p.epi.act);
+      activate(v, p.epi.act);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        v[j][0] += bf16_lo(res[j].x); v[j][1] += bf16_hi(res[j].x); v[j][2] += bf16_lo(res[j].y); v[j][3] += bf16_hi(res[j].y);
+        v[4 * j] += bf16_lo(res[j].x); v[4 * j + 1] += bf16_hi(res[j].x);
+        v[4 * j + 2] += bf16_lo(res[j].y); v[4 * j + 3] += bf16_hi(res[j].y);
         if (in[j])
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + m * p.epi.ldy + col + 128 * j) =
-              make_uint2(pack_bf16x2(v[j][0], v[j][1]), pack_bf16x2(v[j][2], v[j][3]));
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + (size_t)(mt * BM + r) * p.epi.ldy + col + 128 * j) =
+              make_uint2(pack_bf16x2(v[4 * j], v[4 * j + 1]), pack_bf16x2(v[4 * j + 2], v[4 * j + 3]));
+        f[j] = fn[j];
+        res[j] = rn[j];
       }
     }
-    w4a16::cluster_arrive();                                  // nobody reads this CTA's sums any more
-    w4a16::cluster_wait();
+    if (slices > 1) {                                           // nobody reads this CTA's sums any more
+      w4a16::cluster_arrive();
+      w4a16::cluster_wait();
+    }
   }
 }
 
