@@ -14,7 +14,7 @@ product without its BF16 rounding), the result differs from y by at most
     L e  +  1e-5 |act|  +  2^-23 (|z| + |act| + |y|)  +  2^-8 |y + those|
 
 L = 1.13 bounds |act'| of every activation here (gelu: 1.1290, gelu_tanh:
-1.1290, silu: 1.0998), 1e-5 |act| covers the fast exponential and division, the
+1.1290, silu: 1.0998), 1e-5 |act| covers the fast exponential and reciprocal, the
 2^-23 terms the FP32 sums, and 2^-8 |.| half a BF16 step.
 """
 from __future__ import annotations

@@ -17,7 +17,7 @@ which covers tensor-core additions that truncate):
     within a group, K / 128 over the groups, 16 over warps and 148 over CTAs, so it is
     off by at most d(K) u A with d(K) = 172 + K / 128;
   * h = w silu(g) u with |silu'| <= 1.1: off by |w| (1.1 e_g |u| + |silu(g)| e_u +
-    1.1 e_g e_u) + 1e-5 |h| (fast exponential and division) + 2^-16 |h| (two BF16
+    1.1 e_g e_u) + 1e-5 |h| (fast exponential and reciprocal) + 2^-16 |h| (two BF16
     numbers, each rounding at most half a step of 2^-7);
   * down: |Wd| e_h summed, its own additions d(I topk) u over A' = 8 sum |h| s, and the
     residual;

@@ -16,18 +16,29 @@ struct EpiParams {
   uint32_t act;
 };
 
-// v * sigmoid(s).  The fast exponential and division are good to about 1e-6
-// relative, far inside the 2^-9 of the BF16 rounding that follows.  For s so
-// negative that 1 + exp(-s) leaves the division's range the result is 0, the
-// limit (|v sigmoid(s)| < 1e-36 there).
-__device__ __forceinline__ float times_sigmoid(float v, float s) { return __fdividef(v, 1.0f + __expf(-s)); }
+// v / (1 + 2^t) = v * sigmoid(-t ln 2), by the hardware's approximate power of two and
+// reciprocal (two units in the last place together).  Rounding t costs |t| 2^-24: about
+// 1e-5 relative where the result has not vanished next to 1e-36, far inside the 2^-9 of
+// the BF16 rounding that follows.  2^t = inf gives 0, the limit.
+__device__ __forceinline__ float over_one_plus_exp2(float v, float t) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return v * r;
+}
+constexpr float kNegLog2E = -1.4426950408889634f;
+// v * sigmoid(s)
+__device__ __forceinline__ float times_sigmoid(float v, float s) { return over_one_plus_exp2(v, s * kNegLog2E); }
 
 template <uint32_t ACT>
 __device__ __forceinline__ float activate_as(float v) {
   if constexpr (ACT == kActRelu) return v < 0.f ? 0.f : v;                        // NaN stays NaN
   if constexpr (ACT == kActGelu) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
   // 0.5 (1 + tanh(z)) = sigmoid(2 z), z = sqrt(2 / pi) (v + 0.044715 v^3)
-  if constexpr (ACT == kActGeluTanh) return times_sigmoid(v, 1.5957691216057308f * __fmaf_rn(0.044715f * v * v, v, v));
+  if constexpr (ACT == kActGeluTanh) {
+    constexpr float a = kNegLog2E * 1.5957691216057308f, b = a * 0.044715f;
+    return over_one_plus_exp2(v, v * __fmaf_rn(b, v * v, a));
+  }
   if constexpr (ACT == kActSilu) return times_sigmoid(v, v);
   return v;
 }
