@@ -441,8 +441,9 @@ def nvfp4_gemm_w4a4_epilogue(xq, wq, M: int, N: int, K: int, *, bias=None, activ
 
     xq / wq: (codes, scales, t) of nvfp4_quantize.  bias: [N] bf16; activation:
     a name of ACTIVATIONS; residual: [M, N] bf16.  residual and y may be views
-    with contiguous rows (a row stride that is a multiple of 8), and residual
-    may be y: the residual stream updated in place."""
+    with contiguous rows (a row stride of at least N that is a multiple of 8, so
+    no broadcast rows), and residual may be y: the residual stream updated in
+    place."""
     return _call("nvfp4_gemm_w4a4_epilogue", stream, xq[0], xq, wq, M, N, K, bias, _activation(activation),
                  residual, y)
 

@@ -49,6 +49,17 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
+// A matrix whose rows share memory (a broadcast one has a row stride of 0, which the C
+// calls take for "N") is no residual and no output.  Looked at before the device is, so
+// that it can be without one.
+void rows_apart(PyObject* o, const char* name) {
+  if (o == Py_None) return;
+  const at::Tensor& t = tensor(o, name);
+  if (t.dim() == 2 && t.size(0) > 1 && t.stride(0) < t.size(1))
+    throw Bad{std::string(name) + " must have a row stride of at least " + std::to_string(t.size(1)) + ", not " +
+              std::to_string(t.stride(0)) + " (broadcast rows have to be copied)"};
+}
+
 // One call: the device of its first tensor, made current, and that device's stream.
 struct Call {
   c10::cuda::OptionalCUDAGuard guard;
@@ -78,7 +89,7 @@ struct Call {
       throw Bad{std::string(name) + " must be contiguous of shape " + shown(shape) + ", not " + shown(t.sizes())};
     return t.data_ptr();
   }
-  // A BF16 [M, N] matrix with contiguous rows; ld: its row stride (0: N).
+  // A BF16 [M, N] matrix with contiguous rows that are apart (rows_apart); ld: its row stride (0, for one row: N).
   void* rows(const at::Tensor& t, const char* name, int64_t M, int64_t N, int64_t& ld) const {
     fits(t, name, at::kBFloat16);
     if (t.dim() != 2 || t.size(0) != M || t.size(1) != N)
@@ -177,6 +188,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
 
 // xq, wq, M, N, K, bias, activation, residual, y
 PyObject* w4a4(PyObject* const* a) {
+  rows_apart(a[7], "residual");
+  rows_apart(a[8], "y");
   const int64_t M = integer(a[2]), N = integer(a[3]), K = integer(a[4]);
   const Pair q(a[0], "xq", 3);
   const Call c(*q.codes);
@@ -190,6 +203,8 @@ PyObject* w4a4(PyObject* const* a) {
 
 // x, (packed_codes, packed_scales), N, bias, activation, residual, y
 PyObject* w4a16(PyObject* const* a) {
+  rows_apart(a[5], "residual");
+  rows_apart(a[6], "y");
   const at::Tensor& x = tensor(a[0], "x");
   const Call c(x);
   if (x.dim() != 2) throw Bad{"x must be [M, K]"};
@@ -205,6 +220,8 @@ PyObject* w4a16(PyObject* const* a) {
 
 // x, w4a4, w4a16, N, bias, activation, residual, crossover_m, y, workspace
 PyObject* linear(PyObject* const* a) {
+  rows_apart(a[6], "residual");
+  rows_apart(a[8], "y");
   const at::Tensor& x = tensor(a[0], "x");
   const Call c(x);
   if (x.dim() != 2) throw Bad{"x must be [M, K]"};

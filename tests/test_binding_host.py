@@ -1,0 +1,42 @@
+"""What the compiled binding refuses by the arguments' form alone, before it looks at a device (no GPU)."""
+import pytest
+import torch
+
+import phase_disaggregated_quantized_b200 as nvq
+from phase_disaggregated_quantized_b200 import build_lib
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build_lib.build()
+
+
+def _bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def products(M, N, K):
+    """The three calls with an epilogue on host tensors, which each refuses in the end for being there."""
+    x, u8, t = _bf16(M, K), torch.zeros(8, dtype=torch.uint8), torch.zeros(1)
+    yield lambda **kw: nvq.nvfp4_gemm_w4a4_epilogue((u8, u8, t), (u8, u8, t), M, N, K, **kw)
+    yield lambda **kw: nvq.w4a16_gemm_epilogue(x, u8, u8, N, **kw)
+    yield lambda **kw: nvq.nvq_linear_epilogue(x, None, (u8, u8), N, **kw)
+
+
+@pytest.mark.parametrize("name", ["residual", "y"])
+def test_rows_that_share_memory_are_refused(name):
+    """Strides of 0 (broadcast) and of less than a row; (0, 1) is what expand gives."""
+    N = 32
+    assert _bf16(1, N).expand(4, N).stride() == (0, 1)
+    for shared in (_bf16(1, N).expand(4, N), _bf16(N).expand(4, N), _bf16(4 * N).as_strided((4, N), (N - 8, 1)),
+                   _bf16(4 * N).as_strided((4, N), (8, 1)), _bf16(1, 1).expand(4, N)):
+        for call in products(4, N, 128):
+            with pytest.raises(ValueError, match="row stride of at least 32"):
+                call(**{name: shared})
+    for apart in (_bf16(4, N), _bf16(4, 3 * N)[:, 8:8 + N], _bf16(8, N)[::2]):
+        for call in products(4, N, 128):
+            with pytest.raises(ValueError, match="CUDA"):
+                call(**{name: apart})
+    for call in products(1, N, 128):                         # one row has no row stride
+        with pytest.raises(ValueError, match="CUDA"):
+            call(**{name: _bf16(1, 1).expand(1, N)})

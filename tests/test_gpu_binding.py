@@ -1,0 +1,53 @@
+"""The compiled binding on the GPU: arguments it must refuse before anything is launched, and how it calls."""
+import pytest
+import torch
+
+import phase_disaggregated_quantized_b200 as nvq
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from phase_disaggregated_quantized_b200 import build_lib
+    build_lib.build()
+    nvq.lib()
+    yield
+    nvq.check_device_error()
+
+
+def products(M, N, K, seed=0):
+    """The calls with an epilogue, by both paths of the dispatch."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16).cuda()
+    w = torch.randn(N, K, generator=g).to(torch.bfloat16).cuda()
+    i4, f4, xq = nvq.int4_pack_weights(*nvq.int4_quantize(w), N, K), nvq.nvfp4_quantize(w), nvq.nvfp4_quantize(x)
+    return [lambda **kw: nvq.nvfp4_gemm_w4a4_epilogue(xq, f4, M, N, K, **kw),
+            lambda **kw: nvq.w4a16_gemm_epilogue(x, *i4, N, **kw),
+            lambda **kw: nvq.nvq_linear_epilogue(x, f4, i4, N, crossover_m=10 ** 6, **kw),
+            lambda **kw: nvq.nvq_linear_epilogue(x, f4, i4, N, crossover_m=0, **kw)]
+
+
+@pytest.mark.parametrize("M", [2, 4, 9, 40, 200])
+def test_broadcast_rows_are_refused_and_their_copy_is_not(M):
+    N = 64
+    row = torch.randn(1, N, generator=torch.Generator().manual_seed(M)).to(torch.bfloat16).cuda()
+    before = row.clone()
+    for call in products(M, N, 128):
+        for kw in (dict(residual=row.expand(M, N)), dict(y=row.expand(M, N)),
+                   dict(residual=row.expand(M, N), y=torch.empty(M, N, dtype=torch.bfloat16, device="cuda"))):
+            with pytest.raises(ValueError, match="row stride of at least 64"):
+                call(**kw)
+        # the sum with its copy is the sum with the row as a bias: both are added in FP32, to a product of one rounding
+        assert torch.equal(call(residual=row.expand(M, N).contiguous()), call(bias=row[0]))
+    assert torch.equal(row, before)
+
+
+def test_one_row_may_be_broadcast():
+    """A single row has no row stride: whatever the view says of it, N elements are there."""
+    N = 64
+    for call in products(1, N, 128):
+        wide = torch.randn(N, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+        assert torch.equal(call(residual=wide.expand(1, N)), call(bias=wide))
