@@ -307,10 +307,10 @@ PyObject* route(PyObject* const* a) {
 
 // x, ids, weights, gate_up, down, E, I, residual, y, workspace
 PyObject* experts(PyObject* const* a) {
-  const at::Tensor& x = tensor(a[0], "x");
+  const at::Tensor &x = tensor(a[0], "x"), &ids = tensor(a[1], "ids");
+  tensor(a[2], "weights");                         // an input here: Choices would make one
   const Call c(x);
   const Tokens t(c, x);
-  const at::Tensor& ids = tensor(a[1], "ids");
   if (ids.dim() != 2) throw Bad{"ids must be [T, topk]"};
   const int64_t topk = ids.size(1), E = integer(a[5]), I = integer(a[6]);
   const Choices k(c, a[1], a[2], t.T, topk);

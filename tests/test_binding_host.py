@@ -40,3 +40,16 @@ def test_rows_that_share_memory_are_refused(name):
     for call in products(1, N, 128):                         # one row has no row stride
         with pytest.raises(ValueError, match="CUDA"):
             call(**{name: _bf16(1, 1).expand(1, N)})
+
+
+def test_experts_take_no_missing_choices():
+    """ids and weights are inputs of the experts: nothing stands in for them (moe_route makes them where they are outputs)."""
+    x, u8 = _bf16(2, 128), torch.zeros(8, dtype=torch.uint8)
+    ids, weights = torch.zeros(2, 1, dtype=torch.int32), torch.ones(2, 1)
+    call = lambda i, w: nvq.w4a16_moe_experts(x, i, w, (u8, u8), (u8, u8), 2, 128)             # noqa: E731
+    with pytest.raises(ValueError, match="weights must be a tensor"):
+        call(ids, None)
+    with pytest.raises(ValueError, match="ids must be a tensor"):
+        call(None, weights)
+    with pytest.raises(ValueError, match="CUDA"):
+        call(ids, weights)

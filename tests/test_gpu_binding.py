@@ -51,3 +51,16 @@ def test_one_row_may_be_broadcast():
     for call in products(1, N, 128):
         wide = torch.randn(N, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
         assert torch.equal(call(residual=wide.expand(1, N)), call(bias=wide))
+
+
+def test_experts_take_no_missing_choices():
+    E, H, I = 2, 128, 128
+    pack = lambda r, c: nvq.int4_pack_weights(*nvq.int4_quantize(torch.ones(r, c, dtype=torch.bfloat16).cuda()), r, c)   # noqa: E731
+    gate_up, down = pack(E * 2 * I, H), pack(E * H, I)
+    x, ids = torch.ones(3, H, dtype=torch.bfloat16).cuda(), torch.zeros(3, 1, dtype=torch.int32).cuda()
+    y = torch.full((3, H), 7.0, dtype=torch.bfloat16).cuda()
+    with pytest.raises(ValueError, match="weights must be a tensor"):
+        nvq.w4a16_moe_experts(x, ids, None, gate_up, down, E, I, y=y)
+    with pytest.raises(ValueError, match="ids must be a tensor"):
+        nvq.w4a16_moe_experts(x, None, torch.ones(3, 1).cuda(), gate_up, down, E, I, y=y)
+    assert (y == 7).all()
