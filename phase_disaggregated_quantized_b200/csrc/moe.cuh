@@ -147,7 +147,7 @@ __device__ __forceinline__ void select_experts(const float* l, uint32_t planes, 
 // tokens are spread over clusters of eight as long as the device holds those at once.
 template <int NTK>
 __global__ void __launch_bounds__(RTHREADS, 1)
-route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ wr, uint32_t T, uint32_t E,
+route_kernel(const __nv_bfloat16* x, const __nv_bfloat16* __restrict__ wr, uint32_t T, uint32_t E,
              uint32_t H, uint32_t topk, uint32_t renorm, int32_t* __restrict__ ids, float* __restrict__ weights) {
   extern __shared__ __align__(16) float rsm[];
   using S = RouteShape<NTK>;
@@ -201,7 +201,7 @@ route_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restric
     for (uint32_t i = threadIdx.x; i < nt * row4; i += RTHREADS) {
       const uint32_t t = i / row4, w = i - t * row4;
       *reinterpret_cast<uint4*>(xs + t * RXROW + w * 16) =
-          reinterpret_cast<const uint4*>(x + (size_t)(t0 + t) * H + (size_t)c0 * 64)[w];
+          __ldcg(reinterpret_cast<const uint4*>(x + (size_t)(t0 + t) * H + (size_t)c0 * 64) + w);   // may have been written since the launch
     }
     __syncthreads();
     float acc[NTK][4] = {};
@@ -888,13 +888,14 @@ __global__ void __launch_bounds__(W * 32, 16 / W) down_kernel(const ExpertParams
   float* rows = sums + warp * outs;
   const uint32_t wlog = half ? 4 : 5;
   auto output_at = [&](uint32_t n, uint32_t i) { return (size_t)(i >> wlog) * H + n * width + (i & (width - 1)); };
-  // The residual of this thread's outputs of tile n (requested, not yet waited for).
+  // The residual of this thread's outputs of tile n (requested, not yet waited for; final
+  // as ids and weights are, and read past L1 as they are).
   auto residual_of = [&](uint32_t n, uint16_t (&r)[OUTS]) {
     if (p.residual)
 #pragma unroll
       for (int k = 0; k < OUTS; ++k) {
         const uint32_t i = threadIdx.x + k * THREADS;
-        if (i < outs) r[k] = reinterpret_cast<const uint16_t*>(p.residual)[output_at(n, i)];
+        if (i < outs) r[k] = __ldcg(reinterpret_cast<const uint16_t*>(p.residual) + output_at(n, i));
       }
   };
   auto store = [&](uint32_t n, uint32_t i, float v, uint16_t r) {

@@ -414,7 +414,7 @@ __device__ __forceinline__ void sparse_unit(uint32_t unit, uint32_t lane, const 
 #pragma unroll
     for (int t = 0; t < NT8; ++t) {
       const uint4* px = xrow[t] + gk * 16u + 4u * st + 2u * (c >> 1);   // rows >= M read row 0 (discarded)
-      const uint4 x0 = __ldg(px), x1 = __ldg(px + 1);
+      const uint4 x0 = px[0], x1 = px[1];
       b[t][0] = odd ? x0.y : x0.x;
       b[t][1] = odd ? x0.w : x0.z;
       b[t][2] = odd ? x1.y : x1.x;
@@ -433,9 +433,11 @@ __device__ __forceinline__ void sparse_unit(uint32_t unit, uint32_t lane, const 
 }
 
 // EPI: bias, activation and residual where a tile is stored (ep; not read otherwise).
+// x is not __restrict__ and read by ordinary loads: this kernel may start before x is
+// written, so x is no constant of the launch as the packed weights are.
 template <int NT8, bool SPARSE, bool EPI>
 __global__ void __launch_bounds__(Cfg<NT8, SPARSE>::THREADS, Cfg<NT8, SPARSE>::MIN_CTAS) w4a16_kernel(
-    const __nv_bfloat16* __restrict__ x, const uint8_t* __restrict__ pcodes, const uint8_t* __restrict__ pscales,
+    const __nv_bfloat16* x, const uint8_t* __restrict__ pcodes, const uint8_t* __restrict__ pscales,
     __nv_bfloat16* y, uint32_t M, uint32_t N, uint32_t K, const EpiParams ep) {
   using C = Cfg<NT8, SPARSE>;
   using U = typename C::U;
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(Cfg<NT8, SPARSE>::THREADS, Cfg<NT8, SPARSE>::M
       for (int t = 0; t < NT8; ++t)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          xa[t][v] = (!SPARSE && C::XDB) ? __ldg(xrow[t] + g_first * 16u + v) : make_uint4(0, 0, 0, 0);
+          xa[t][v] = (!SPARSE && C::XDB) ? xrow[t][g_first * 16u + v] : make_uint4(0, 0, 0, 0);
           xb[t][v] = make_uint4(0, 0, 0, 0);
         }
       uint32_t nt = wt_first, g = g_first, left = nf;
@@ -569,14 +571,14 @@ __global__ void __launch_bounds__(Cfg<NT8, SPARSE>::THREADS, Cfg<NT8, SPARSE>::M
               for (int t = 0; t < NT8; ++t)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                  nxt[t][v] = __ldg(xrow[t] + gn * 16u + v);      // rows >= M read row 0 (discarded)
+                  nxt[t][v] = xrow[t][gn * 16u + v];      // rows >= M read row 0 (discarded)
               dense_unit<NT8, C::ONES, C::LATE>(stage + i * UC + lane * 16, cur, d);
             } else {
 #pragma unroll
               for (int t = 0; t < NT8; ++t)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                  xa[t][v] = __ldg(xrow[t] + (g + i) * 16u + v);
+                  xa[t][v] = xrow[t][(g + i) * 16u + v];
               dense_unit<NT8, C::ONES, C::LATE>(stage + i * UC + lane * 16, xa, d);
             }
             // Scale word tt of this lane: rows 16 tt + g (low half) and 16 tt + g + 8 (high half).
