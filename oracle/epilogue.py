@@ -26,7 +26,7 @@ import numpy as np
 ACTIVATIONS = ("none", "relu", "gelu", "gelu_tanh", "silu")
 MAX_SLOPE = 1.13
 
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 def activation(z: np.ndarray, name: str) -> np.ndarray:
@@ -37,7 +37,7 @@ def activation(z: np.ndarray, name: str) -> np.ndarray:
         if name == "relu":
             return np.where(z < 0, 0.0, z)
         if name == "gelu":
-            return 0.5 * z * (1 + _erf(z / math.sqrt(2)))
+            return 0.5 * z * _erfc(-z / math.sqrt(2))             # 1 + erf(u) = erfc(-u), without its cancellation
         if name == "gelu_tanh":
             return 0.5 * z * (1 + np.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)))
         if name == "silu":

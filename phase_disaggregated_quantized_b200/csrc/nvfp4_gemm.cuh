@@ -605,7 +605,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
             f[0] += bf16_lo(b.x); f[1] += bf16_hi(b.x); f[2] += bf16_lo(b.y); f[3] += bf16_hi(b.y);
             f[4] += bf16_lo(b.z); f[5] += bf16_hi(b.z); f[6] += bf16_lo(b.w); f[7] += bf16_hi(b.w);
           }
-          activate(f, p.epi.act);
+          activate<true>(f, p.epi.act);
           // 128-byte swizzle: 16-byte chunk e of row r sits at chunk e ^ (r & 7).
           uint4* cell = reinterpret_cast<uint4*>(cbuf + lane * 128u + ((uint32_t)e ^ (lane & 7u)) * 16u);
           if (res) {
@@ -775,7 +775,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_const
         v[4 * j] += bf16_lo(bias[j].x); v[4 * j + 1] += bf16_hi(bias[j].x);
         v[4 * j + 2] += bf16_lo(bias[j].y); v[4 * j + 3] += bf16_hi(bias[j].y);
       }
-      activate(v, p.epi.act);
+      activate<false>(v, p.epi.act);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         v[4 * j] += bf16_lo(res[j].x); v[4 * j + 1] += bf16_hi(res[j].x);

@@ -297,7 +297,7 @@ __device__ __forceinline__ void store_tile(__nv_bfloat16* y, const float (&acc)[
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += (e & 2) ? b_hi : b_lo;
-        activate(v, ep.act);
+        activate<false>(v, ep.act);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += r[e];
       }

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(THREADS, 1) gemm_kernel(const Params p) {
             const uint2 b = *reinterpret_cast<const uint2*>(p.ep.bias + n);
             v[0] += bf16_lo(b.x); v[1] += bf16_hi(b.x); v[2] += bf16_lo(b.y); v[3] += bf16_hi(b.y);
           }
-          activate(v, p.ep.act);
+          activate<true>(v, p.ep.act);
           if (p.ep.residual != nullptr) {
             v[0] += bf16_lo(res[j].x); v[1] += bf16_hi(res[j].x); v[2] += bf16_lo(res[j].y); v[3] += bf16_hi(res[j].y);
           }
