@@ -721,9 +721,11 @@ __global__ void __launch_bounds__(W * 32, 16 / W) gate_up_kernel(const ExpertPar
           for (int r = 0; r < 2; ++r) {
             const float gate = 4.f * acc[0][2 * r + k], up = 4.f * acc[1][2 * r + k], h = times_sigmoid(gate, gate) * up * w;
             // Two BF16 halves carry h to 16 bits: one would add an error as large as the rounding of y.
+            // An infinite half stands alone: h less itself is NaN.
             const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+            const float top = __bfloat162float(hi);
             to[32 * r] = hi;
-            to[32 * r + low] = __float2bfloat16_rn(h - __bfloat162float(hi));
+            to[32 * r + low] = __float2bfloat16_rn(isinf(top) ? 0.f : h - top);
           }
         }
     };
