@@ -37,6 +37,7 @@ struct Entry {
 struct Bad {            // becomes a ValueError
   std::string what;
 };
+struct Raised {};       // Python's own error is set
 
 std::string shown(c10::IntArrayRef s) {
   std::string r = "[";
@@ -115,6 +116,12 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};                       // an object without a truth value
+  return v;
+}
+
 struct Pair {           // (codes, scales) or (codes, scales, t)
   const at::Tensor *codes, *scales, *t;
   Pair(PyObject* o, const char* name, Py_ssize_t n) {
@@ -178,6 +185,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
   try {
     return F(args);
+  } catch (const Raised&) {
   } catch (const Bad& b) {
     PyErr_SetString(PyExc_ValueError, b.what.c_str());
   } catch (...) {                                  // torch's own errors, out of memory among them
@@ -294,6 +302,7 @@ int64_t small_count(PyObject* o) {                 // topk: an int in the C call
 
 // x, w_router, topk, renormalize, ids, weights
 PyObject* route(PyObject* const* a) {
+  const int renormalize = truth(a[3]);
   const at::Tensor &x = tensor(a[0], "x"), &wr = tensor(a[1], "w_router");
   const Call c(x);
   const Tokens t(c, x);
@@ -301,7 +310,7 @@ PyObject* route(PyObject* const* a) {
   const int64_t E = wr.size(0), topk = small_count(a[2]);
   const void* rp = c.exact(wr, "w_router", at::kBFloat16, {E, t.H});
   const Choices k(c, a[4], a[5], t.T, topk);
-  const nvq_status s = g.route(t.x, rp, t.T, E, t.H, (int)topk, PyObject_IsTrue(a[3]), k.ip, k.wp, c.stream());
+  const nvq_status s = g.route(t.x, rp, t.T, E, t.H, (int)topk, renormalize, k.ip, k.wp, c.stream());
   return s == NVQ_OK ? tuple_of({k.ids, k.weights}) : status(s);
 }
 
@@ -323,6 +332,7 @@ PyObject* experts(PyObject* const* a) {
 
 // x, w_router, gate_up, down, I, topk, renormalize, residual, ids, weights, y, workspace
 PyObject* moe(PyObject* const* a) {
+  const int renormalize = truth(a[6]);
   const at::Tensor &x = tensor(a[0], "x"), &wr = tensor(a[1], "w_router");
   const Call c(x);
   const Tokens t(c, x);
@@ -332,7 +342,7 @@ PyObject* moe(PyObject* const* a) {
   const Choices k(c, a[8], a[9], t.T, topk);
   const Layer l(c, a[2], a[3], a[7], a[10], a[11], t.T, E, t.H, I, topk);
   const nvq_status s = g.moe(t.x, rp, l.gate_up.codes, l.gate_up.scales, l.down.codes, l.down.scales, l.rp, l.yp, k.ip,
-                             k.wp, t.T, E, t.H, I, (int)topk, PyObject_IsTrue(a[6]), l.wp, l.work.numel(), c.stream());
+                             k.wp, t.T, E, t.H, I, (int)topk, renormalize, l.wp, l.work.numel(), c.stream());
   return s == NVQ_OK ? tuple_of({l.y, k.ids, k.weights}) : status(s);
 }
 

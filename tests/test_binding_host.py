@@ -53,3 +53,18 @@ def test_experts_take_no_missing_choices():
         call(None, weights)
     with pytest.raises(ValueError, match="CUDA"):
         call(ids, weights)
+
+
+def test_renormalize_without_a_truth_value_raises_its_own_error():
+    class Neither:
+        def __bool__(self):
+            raise KeyError("neither")
+
+    x, u8 = _bf16(2, 128), torch.zeros(8, dtype=torch.uint8)
+    for flag, error in ((Neither(), KeyError), (torch.ones(2), RuntimeError)):
+        with pytest.raises(error):
+            nvq.moe_route(x, x, 1, renormalize=flag)
+        with pytest.raises(error):
+            nvq.w4a16_moe(x, x, (u8, u8), (u8, u8), 128, 1, renormalize=flag)
+    with pytest.raises(ValueError, match="CUDA"):
+        nvq.moe_route(x, x, 1, renormalize=torch.ones(1))

@@ -64,3 +64,12 @@ def test_experts_take_no_missing_choices():
     with pytest.raises(ValueError, match="ids must be a tensor"):
         nvq.w4a16_moe_experts(x, None, torch.ones(3, 1).cuda(), gate_up, down, E, I, y=y)
     assert (y == 7).all()
+
+
+def test_renormalize_without_a_truth_value_launches_nothing():
+    x = torch.ones(3, 128, dtype=torch.bfloat16).cuda()
+    ids, weights = torch.full((3, 1), 7, dtype=torch.int32).cuda(), torch.full((3, 1), 7.0).cuda()
+    with pytest.raises(RuntimeError, match="(?i)bool"):
+        nvq.moe_route(x, x, 1, renormalize=torch.ones(2), ids=ids, weights=weights)
+    torch.cuda.synchronize()
+    assert (ids == 7).all() and (weights == 7).all()
