@@ -18,6 +18,7 @@
 #include <exception>
 #include <initializer_list>
 #include <string>
+#include <utility>
 
 #include "../../include/nvq.h"
 
@@ -122,39 +123,55 @@ int truth(PyObject* o) {
   return v;
 }
 
-struct Pair {           // (codes, scales) or (codes, scales, t)
-  const at::Tensor *codes, *scales, *t;
+// The library's call, without the interpreter's lock: a full launch queue makes it wait,
+// and the other Python threads need not.
+template <typename F>
+nvq_status unlocked(F f) {
+  struct Released {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+  } released;
+  return f();
+}
+
+// (codes, scales) or (codes, scales, t), held: they may come in a list that another thread changes meanwhile.
+struct Pair {
+  at::Tensor codes, scales, t;
+  Pair() = default;
   Pair(PyObject* o, const char* name, Py_ssize_t n) {
     if (!(PyTuple_Check(o) || PyList_Check(o)) || PySequence_Fast_GET_SIZE(o) != n)
       throw Bad{std::string(name) + (n == 3 ? " must be (codes, scales, t)" : " must be (packed_codes, packed_scales)")};
     PyObject** v = PySequence_Fast_ITEMS(o);
-    codes = &tensor(v[0], name);
-    scales = &tensor(v[1], name);
-    t = n == 3 ? &tensor(v[2], name) : nullptr;
+    codes = tensor(v[0], name);
+    scales = tensor(v[1], name);
+    if (n == 3) t = tensor(v[2], name);
   }
 };
 
 int64_t tiled_scales(int64_t rows, int64_t K) { return (rows + 127) / 128 * 128 * (K / 16); }
 
 struct Nvfp4 {
-  const uint8_t *codes, *scales;
-  const float* t;
-  Nvfp4(const Call& c, PyObject* o, const char* name, int64_t rows, int64_t K) {
-    const Pair q(o, name, 3);
-    codes = static_cast<uint8_t*>(c.flat(*q.codes, name, at::kByte, rows * (K / 2)));
-    scales = static_cast<uint8_t*>(c.flat(*q.scales, name, at::kByte, tiled_scales(rows, K)));
-    t = static_cast<float*>(c.flat(*q.t, name, at::kFloat, 1));
+  Pair q;
+  const uint8_t *codes = nullptr, *scales = nullptr;
+  const float* t = nullptr;
+  Nvfp4(const Call& c, Pair held, const char* name, int64_t rows, int64_t K) : q(std::move(held)) {
+    codes = static_cast<uint8_t*>(c.flat(q.codes, name, at::kByte, rows * (K / 2)));
+    scales = static_cast<uint8_t*>(c.flat(q.scales, name, at::kByte, tiled_scales(rows, K)));
+    t = static_cast<float*>(c.flat(q.t, name, at::kFloat, 1));
   }
+  Nvfp4(const Call& c, PyObject* o, const char* name, int64_t rows, int64_t K) : Nvfp4(c, Pair(o, name, 3), name, rows, K) {}
+  Nvfp4() = default;      // none
 };
 
 struct Int4 {
-  const uint8_t* codes;
-  const void* scales;
-  Int4(const Call& c, PyObject* o, const char* name, int64_t rows, int64_t K) {
-    const Pair q(o, name, 2);
-    codes = static_cast<uint8_t*>(c.flat(*q.codes, name, at::kByte, rows * K / 2));
-    scales = c.flat(*q.scales, name, at::kByte, rows * (K / 128) * 2);
+  Pair q;
+  const uint8_t* codes = nullptr;
+  const void* scales = nullptr;
+  Int4(const Call& c, PyObject* o, const char* name, int64_t rows, int64_t K) : q(o, name, 2) {
+    codes = static_cast<uint8_t*>(c.flat(q.codes, name, at::kByte, rows * K / 2));
+    scales = c.flat(q.scales, name, at::kByte, rows * (K / 128) * 2);
   }
+  Int4() = default;       // none
 };
 
 nvq_epilogue epilogue(const Call& c, PyObject* bias, PyObject* act, PyObject* residual, const at::Tensor& y, int64_t M,
@@ -199,13 +216,13 @@ PyObject* w4a4(PyObject* const* a) {
   rows_apart(a[7], "residual");
   rows_apart(a[8], "y");
   const int64_t M = integer(a[2]), N = integer(a[3]), K = integer(a[4]);
-  const Pair q(a[0], "xq", 3);
-  const Call c(*q.codes);
-  const Nvfp4 x(c, a[0], "xq", M, K), w(c, a[1], "wq", N, K);
+  Pair xq(a[0], "xq", 3);
+  const Call c(xq.codes);
+  const Nvfp4 x(c, std::move(xq), "xq", M, K), w(c, a[1], "wq", N, K);
   const at::Tensor y = c.given_or(a[8], "y", {M, N}, at::kBFloat16);
   void* yp;
   const nvq_epilogue e = epilogue(c, a[5], a[6], a[7], y, M, N, &yp);
-  const nvq_status s = g.w4a4(x.codes, x.scales, x.t, w.codes, w.scales, w.t, yp, M, N, K, &e, c.stream());
+  const nvq_status s = unlocked([&] { return g.w4a4(x.codes, x.scales, x.t, w.codes, w.scales, w.t, yp, M, N, K, &e, c.stream()); });
   return s == NVQ_OK ? THPVariable_Wrap(y) : status(s);
 }
 
@@ -222,7 +239,7 @@ PyObject* w4a16(PyObject* const* a) {
   const at::Tensor y = c.given_or(a[6], "y", {M, N}, at::kBFloat16);
   void* yp;
   const nvq_epilogue e = epilogue(c, a[3], a[4], a[5], y, M, N, &yp);
-  const nvq_status s = g.w4a16(xp, w.codes, w.scales, yp, M, N, K, &e, c.stream());
+  const nvq_status s = unlocked([&] { return g.w4a16(xp, w.codes, w.scales, yp, M, N, K, &e, c.stream()); });
   return s == NVQ_OK ? THPVariable_Wrap(y) : status(s);
 }
 
@@ -235,26 +252,17 @@ PyObject* linear(PyObject* const* a) {
   if (x.dim() != 2) throw Bad{"x must be [M, K]"};
   const int64_t M = x.size(0), K = x.size(1), N = integer(a[3]), crossover = integer(a[7]);
   const void* xp = c.flat(x, "x", at::kBFloat16, 0);
-  const uint8_t *wc = nullptr, *ws = nullptr, *pc = nullptr;
-  const float* wt = nullptr;
-  const void* ps = nullptr;
-  if (a[1] != Py_None) {
-    const Nvfp4 w(c, a[1], "w4a4", N, K);
-    wc = w.codes;
-    ws = w.scales;
-    wt = w.t;
-  }
-  if (a[2] != Py_None) {
-    const Int4 w(c, a[2], "w4a16", N, K);
-    pc = w.codes;
-    ps = w.scales;
-  }
+  const Nvfp4 w4a4 = a[1] == Py_None ? Nvfp4() : Nvfp4(c, a[1], "w4a4", N, K);
+  const Int4 w4a16 = a[2] == Py_None ? Int4() : Int4(c, a[2], "w4a16", N, K);
   const at::Tensor y = c.given_or(a[8], "y", {M, N}, at::kBFloat16);
   const at::Tensor work = c.given_or(a[9], "workspace", {(int64_t)g.linear_bytes(M, N, K, crossover)}, at::kByte);
   void* wp = c.flat(work, "workspace", at::kByte, 0);
   void* yp;
   const nvq_epilogue e = epilogue(c, a[4], a[5], a[6], y, M, N, &yp);
-  const nvq_status s = g.linear(xp, M, N, K, wc, ws, wt, pc, ps, crossover, yp, &e, wp, work.numel(), c.stream());
+  const nvq_status s = unlocked([&] {
+    return g.linear(xp, M, N, K, w4a4.codes, w4a4.scales, w4a4.t, w4a16.codes, w4a16.scales, crossover, yp, &e, wp, work.numel(),
+                    c.stream());
+  });
   return s == NVQ_OK ? THPVariable_Wrap(y) : status(s);
 }
 
@@ -310,7 +318,7 @@ PyObject* route(PyObject* const* a) {
   const int64_t E = wr.size(0), topk = small_count(a[2]);
   const void* rp = c.exact(wr, "w_router", at::kBFloat16, {E, t.H});
   const Choices k(c, a[4], a[5], t.T, topk);
-  const nvq_status s = g.route(t.x, rp, t.T, E, t.H, (int)topk, renormalize, k.ip, k.wp, c.stream());
+  const nvq_status s = unlocked([&] { return g.route(t.x, rp, t.T, E, t.H, (int)topk, renormalize, k.ip, k.wp, c.stream()); });
   return s == NVQ_OK ? tuple_of({k.ids, k.weights}) : status(s);
 }
 
@@ -325,8 +333,10 @@ PyObject* experts(PyObject* const* a) {
   const Choices k(c, a[1], a[2], t.T, topk);
   if (topk > 1 << 20) throw Bad{"topk out of range"};
   const Layer l(c, a[3], a[4], a[7], a[8], a[9], t.T, E, t.H, I, topk);
-  const nvq_status s = g.experts(t.x, k.ip, k.wp, l.gate_up.codes, l.gate_up.scales, l.down.codes, l.down.scales, l.rp,
-                                 l.yp, t.T, E, t.H, I, (int)topk, l.wp, l.work.numel(), c.stream());
+  const nvq_status s = unlocked([&] {
+    return g.experts(t.x, k.ip, k.wp, l.gate_up.codes, l.gate_up.scales, l.down.codes, l.down.scales, l.rp, l.yp, t.T, E, t.H, I,
+                     (int)topk, l.wp, l.work.numel(), c.stream());
+  });
   return s == NVQ_OK ? THPVariable_Wrap(l.y) : status(s);
 }
 
@@ -341,8 +351,10 @@ PyObject* moe(PyObject* const* a) {
   const void* rp = c.exact(wr, "w_router", at::kBFloat16, {E, t.H});
   const Choices k(c, a[8], a[9], t.T, topk);
   const Layer l(c, a[2], a[3], a[7], a[10], a[11], t.T, E, t.H, I, topk);
-  const nvq_status s = g.moe(t.x, rp, l.gate_up.codes, l.gate_up.scales, l.down.codes, l.down.scales, l.rp, l.yp, k.ip,
-                             k.wp, t.T, E, t.H, I, (int)topk, renormalize, l.wp, l.work.numel(), c.stream());
+  const nvq_status s = unlocked([&] {
+    return g.moe(t.x, rp, l.gate_up.codes, l.gate_up.scales, l.down.codes, l.down.scales, l.rp, l.yp, k.ip, k.wp, t.T, E, t.H, I,
+                 (int)topk, renormalize, l.wp, l.work.numel(), c.stream());
+  });
   return s == NVQ_OK ? tuple_of({l.y, k.ids, k.weights}) : status(s);
 }
 

@@ -73,3 +73,53 @@ def test_renormalize_without_a_truth_value_launches_nothing():
         nvq.moe_route(x, x, 1, renormalize=torch.ones(2), ids=ids, weights=weights)
     torch.cuda.synchronize()
     assert (ids == 7).all() and (weights == 7).all()
+
+
+def test_other_threads_run_while_a_call_waits(tmp_path):
+    """A call waits on the host when the launch queue is full.  Here the entry points are a C function that
+    sleeps 0.3 s and refuses, bound into a copy of the module of its own; another thread counts meanwhile."""
+    import ctypes
+    import importlib.util
+    import shutil
+    import subprocess
+    import threading
+    import time
+    src = tmp_path / "slow.c"
+    src.write_text("#include <unistd.h>\nint slow(void) { usleep(300000); return 1; }\nunsigned long none(void) { return 0; }\n")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(tmp_path / "slow.so"), str(src)], check=True)
+    L = ctypes.CDLL(str(tmp_path / "slow.so"))
+    shutil.copy(nvq.BINDING_PATH, tmp_path / "_binding.so")
+    spec = importlib.util.spec_from_file_location("slow._binding", tmp_path / "_binding.so")
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    at = lambda f: ctypes.cast(f, ctypes.c_void_p).value                                       # noqa: E731
+    m.bind(at(L.slow), at(L.slow), at(L.slow), at(L.none), at(L.slow), at(L.none), at(L.slow), at(L.slow))
+    u8 = torch.zeros(1 << 16, dtype=torch.uint8).cuda()
+    x, t, ids, w = torch.zeros(2, 128, dtype=torch.bfloat16).cuda(), torch.zeros(1).cuda(), torch.zeros(2, 1, dtype=torch.int32).cuda(), torch.zeros(2, 1).cuda()
+    q4, p4 = (u8, u8, t), (u8, u8)
+    calls = [lambda: m.nvfp4_gemm_w4a4_epilogue(q4, q4, 2, 64, 128, None, 0, None, None),
+             lambda: m.w4a16_gemm_epilogue(x, p4, 64, None, 0, None, None),
+             lambda: m.nvq_linear_epilogue(x, q4, p4, 64, None, 0, None, -1, None, None),
+             lambda: m.moe_route(x, x, 1, True, None, None),
+             lambda: m.w4a16_moe_experts(x, ids, w, p4, p4, 1, 128, None, None, None),
+             lambda: m.w4a16_moe(x, x[:1], p4, p4, 128, 1, True, None, None, None, None, None)]
+    ticks, stop = [], threading.Event()
+
+    def count():
+        while not stop.is_set():
+            ticks.append(time.perf_counter())
+            time.sleep(0.005)
+
+    thread = threading.Thread(target=count)
+    thread.start()
+    try:
+        for call in calls:
+            begin = time.perf_counter()
+            assert call() == 1
+            end = time.perf_counter()
+            assert end - begin >= 0.29
+            within = [s for s in ticks if begin + 0.05 < s < end - 0.05]
+            assert len(within) >= 5                          # 40 with nothing else to do
+    finally:
+        stop.set()
+        thread.join()
