@@ -419,7 +419,8 @@ nvq_status nvq_linear(const void* x_bf16, int64_t M, int64_t N, int64_t K,
                       void* stream);
 
 /* nvq_linear with an epilogue: the same choice of path, workspace and rules;
- * the product is w4a16_gemm_epilogue or nvfp4_gemm_w4a4_epilogue. */
+ * the product is w4a16_gemm_epilogue or nvfp4_gemm_w4a4_epilogue.  x may not
+ * overlap y, whichever path is taken. */
 nvq_status nvq_linear_epilogue(const void* x_bf16, int64_t M, int64_t N, int64_t K,
                                const uint8_t* w_codes, const uint8_t* w_scales, const float* w_t,
                                const uint8_t* w_packed_codes, const void* w_packed_scales,

@@ -459,7 +459,8 @@ def w4a16_gemm_epilogue(x, packed_codes, packed_scales, N: int, *, bias=None, ac
 
 def nvq_linear_epilogue(x, w4a4=None, w4a16=None, N: int | None = None, *, bias=None, activation: str = "none",
                         residual=None, crossover_m: int = -1, y=None, workspace=None, stream=None):
-    """nvq_linear with bias, activation and residual in the product it picks."""
+    """nvq_linear with bias, activation and residual in the product it picks; x may
+    not overlap y, whichever that is."""
     if N is None:
         raise ValueError("N is required")
     return _call("nvq_linear_epilogue", stream, x, x, w4a4, w4a16, N, bias, _activation(activation),

@@ -1116,6 +1116,9 @@ nvq_status nvq_linear_epilogue(const void* x_bf16, int64_t M, int64_t N, int64_t
   nvq::EpiParams ep;                               // the product's own checks, before anything is enqueued
   nvq_status st = epilogue_params("nvq_linear_epilogue", epilogue, y_bf16, M, N, &ep);
   if (st != NVQ_OK) return st;
+  // This path could allow it, but whether a call is valid must not depend on M.
+  if (spans_meet(bf16_span(x_bf16, M, K, K), bf16_span(y_bf16, M, N, (int64_t)ep.ldy)))
+    return fail(NVQ_ERR_INVALID_ARG, "nvq_linear_epilogue: x overlaps y");
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint8_t* xc = ws + L.codes;
   uint8_t* xs = ws + L.scales;
