@@ -403,6 +403,10 @@ def _load_binding():
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(f"_binding.so not built at {BINDING_PATH}; run "
                                "`python -m phase_disaggregated_quantized_b200.build_lib`")
+        from .build_lib import binding_fits
+        if not binding_fits(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} was built for another torch or Python; run "
+                               "`python -m phase_disaggregated_quantized_b200.build_lib`")
         L = lib()
         spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
         m = importlib.util.module_from_spec(spec)

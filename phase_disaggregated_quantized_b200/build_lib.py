@@ -40,9 +40,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def binding_tag() -> str:
+    """What the binding is compiled against besides its own sources: torch's ABI changes with torch, CPython's with Python."""
+    import torch
+    return (f"nvq binding for torch {torch.__version__} {torch.version.git_version} "
+            f"cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}")
+
+
+def binding_fits(path: str) -> bool:
+    """Whether the binding at `path` carries the tag of the torch and Python that run now."""
+    with open(path, "rb") as f:
+        return binding_tag().encode() + b"\0" in f.read()
+
+
 def build_binding(force: bool = False) -> str:
     header = os.path.join(ROOT, "include", "nvq.h")
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, (BINDING_SOURCE, header))):
+    if not force and os.path.exists(BINDING) and binding_fits(BINDING) \
+            and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, (BINDING_SOURCE, header))):
         return BINDING
     import torch
     root = os.path.dirname(torch.__file__)
@@ -51,9 +65,9 @@ def build_binding(force: bool = False) -> str:
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     lib = os.path.join(root, "lib")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-isystem{d}" for d in inc),
-           BINDING_SOURCE, "-o", BINDING + ".tmp", f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch_python"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DNVQ_BINDING_TAG="{binding_tag()}"',
+           *(f"-isystem{d}" for d in inc), BINDING_SOURCE, "-o", BINDING + ".tmp", f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10",
+           "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     subprocess.run(cmd, check=True)
     os.replace(BINDING + ".tmp", BINDING)
     return BINDING

@@ -394,4 +394,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__binding(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", NVQ_BINDING_TAG) < 0) {   // the build looks for it in the file
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
