@@ -109,27 +109,15 @@ __device__ __forceinline__ void select_topk(const float (&l)[KPL], uint32_t E, u
   weight = e / sum;
 }
 
-// The same with the logits summed over `planes` arrays, `pitch` floats apart.
-// `load` reads one float; the loads of a plane do not wait for one another.
-template <typename Load>
-__device__ __forceinline__ void select_experts(const float* l, uint32_t planes, size_t pitch, Load load, uint32_t E,
-                                               uint32_t topk, bool renorm, uint32_t lane, uint32_t& id, float& weight) {
+// The same from the logits in shared memory, with as many per lane as E takes.
+__device__ __forceinline__ void select_experts(const float* logits, uint32_t E, uint32_t topk, bool renorm, uint32_t lane,
+                                               uint32_t& id, float& weight) {
   auto with = [&](auto kpl) {
     constexpr int KPL = decltype(kpl)::value;
-    float sum[KPL] = {};
-    constexpr uint32_t PL = KPL <= 4 ? 4 : 1;
-    for (uint32_t s = 0; s < planes; s += PL) {
-      float v[PL][KPL];
+    float l[KPL];
 #pragma unroll
-      for (uint32_t k = 0; k < PL; ++k)
-#pragma unroll
-        for (int i = 0; i < KPL; ++i) v[k][i] = s + k < planes && lane + 32 * i < E ? load(l + (s + k) * pitch + lane + 32 * i) : 0.f;
-#pragma unroll
-      for (uint32_t k = 0; k < PL; ++k)
-#pragma unroll
-        for (int i = 0; i < KPL; ++i) sum[i] += v[k][i];
-    }
-    select_topk<KPL>(sum, E, topk, renorm, lane, id, weight);
+    for (int i = 0; i < KPL; ++i) l[i] = 0.f + (lane + 32 * i < E ? logits[lane + 32 * i] : 0.f);   // -0 as 0
+    select_topk<KPL>(l, E, topk, renorm, lane, id, weight);
   };
   if (E <= 128) with(std::integral_constant<int, 4>());
   else if (E <= 256) with(std::integral_constant<int, 8>());
@@ -290,7 +278,7 @@ route_kernel(const __nv_bfloat16* x, const __nv_bfloat16* __restrict__ wr, uint3
     const uint32_t t = t0 + rank + RCS * warp;
     uint32_t id;
     float w;
-    select_experts(l, 1, 0, [](const float* q) { return *q; }, E, topk, renorm != 0, lane, id, w);
+    select_experts(l, E, topk, renorm != 0, lane, id, w);
     if (lane < topk) {
       ids[(size_t)t * topk + lane] = (int32_t)id;
       weights[(size_t)t * topk + lane] = w;
