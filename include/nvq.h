@@ -243,13 +243,16 @@ nvq_status nvfp4_gemm_w4a4_swiglu(const uint8_t* x_codes, const uint8_t* x_scale
  *   NVQ_ACT_GELU       z (1 + erf(z / sqrt 2)) / 2
  *   NVQ_ACT_GELU_TANH  z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
  *   NVQ_ACT_SILU       z / (1 + exp(-z))
+ * Exponentials and reciprocals are the hardware's approximate ones, about 1e-5
+ * relative where it is most; results below about 1e-36 may be 0.
  * bias_bf16        [N] BF16 or NULL, 16-byte aligned.
  * residual_bf16    [M, N] BF16 or NULL, 16-byte aligned.  It may be y itself
  *                  (the same pointer and stride: the residual stream is updated
  *                  in place), or hold other columns of the same buffer; any
  *                  other overlap with y is NVQ_ERR_INVALID_ARG.
  * residual_stride, y_stride: elements from one row to the next, >= N and a
- *                  multiple of 8; 0 means N.
+ *                  multiple of 8; 0 means N (rows that share memory have no form
+ *                  here: one row for all of them is a bias).
  * A NULL nvq_epilogue* (or one of all zeros) is the bare product.
  * ------------------------------------------------------------------------ */
 typedef enum {
@@ -355,9 +358,10 @@ nvq_status w4a16_gemm(const void* x_bf16, const uint8_t* packed_codes, const voi
 /* w4a16_gemm with an epilogue: arguments, shape rules and launch behaviour as
  * there (bias and residual are read after the wait on the preceding kernel; an
  * in-place residual is read once, also in calls of several passes).  For M <= 8
- * the sums are w4a16_gemm's bit for bit; larger M goes through the tcgen05 tensor
- * cores with exact products, FP32 sums and scales in FP32 in an order of its own,
- * fixed by the shapes, and is as fast up to M = 32.  x may not overlap y. */
+ * the sums are w4a16_gemm's bit for bit (so an infinite x gives NaN); larger M goes
+ * through the tcgen05 tensor cores with exact products, FP32 sums and scales in FP32
+ * in an order of its own, fixed by the shapes.  It is made for M <= 32 and handles
+ * larger M 32 rows per pass over W.  x may not overlap y. */
 nvq_status w4a16_gemm_epilogue(const void* x_bf16, const uint8_t* packed_codes, const void* packed_scales,
                                void* y_bf16, int64_t M, int64_t N, int64_t K, const nvq_epilogue* epilogue,
                                void* stream);

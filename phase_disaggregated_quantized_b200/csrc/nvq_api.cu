@@ -1049,6 +1049,9 @@ nvq_status w4a16_moe(const void* x_bf16, const void* w_router_bf16, const uint8_
 // Largest M at which W4A16 beat quantize + W4A4 on B200 for K = 4096, N = 24576
 // with weights read from HBM (profile_case --op crossover: 25.1 vs 28.9 us at
 // M = 16, 39.9 vs 30.0 us at M = 32).
+// nvq_linear_epilogue takes the same one, so that both calls pick alike; its own INT4
+// product stays near or ahead of its W4A4 path up to M = 32 (with a residual: 27.1 vs
+// 26.5 us there, 9.9 vs 16.8 for N = 4096), which crossover_m can say.
 constexpr int64_t kDefaultCrossoverM = 16;
 
 int64_t nvq_default_crossover_m(void) { return kDefaultCrossoverM; }
