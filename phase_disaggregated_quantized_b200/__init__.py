@@ -23,6 +23,7 @@ import ctypes
 import importlib.util
 import os
 import re
+import sysconfig
 
 import torch
 
@@ -396,6 +397,18 @@ def nvq_linear(x, w4a4=None, w4a16=None, N: int | None = None, *, crossover_m: i
 _fast = None
 
 
+def binding_tag() -> str:
+    """What the binding is compiled against besides its own sources: torch's ABI changes with torch, CPython's with Python."""
+    return (f"nvq binding for torch {torch.__version__} {torch.version.git_version} "
+            f"cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}")
+
+
+def binding_fits(path: str) -> bool:
+    """Whether the binding at `path` carries the tag of the torch and Python that run now."""
+    with open(path, "rb") as f:
+        return binding_tag().encode() + b"\0" in f.read()
+
+
 def _load_binding():
     """The compiled binding, bound to the loaded library (raises if it has not been built)."""
     global _fast
@@ -403,7 +416,6 @@ def _load_binding():
         if not os.path.exists(BINDING_PATH):
             raise RuntimeError(f"_binding.so not built at {BINDING_PATH}; run "
                                "`python -m phase_disaggregated_quantized_b200.build_lib`")
-        from .build_lib import binding_fits
         if not binding_fits(BINDING_PATH):
             raise RuntimeError(f"{BINDING_PATH} was built for another torch or Python; run "
                                "`python -m phase_disaggregated_quantized_b200.build_lib`")

@@ -10,6 +10,8 @@ import subprocess
 import sys
 import sysconfig
 
+from . import binding_fits, binding_tag
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libnvq.so")
@@ -38,19 +40,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.replace(LIB + ".tmp", LIB)
     build_binding(force)
     return LIB
-
-
-def binding_tag() -> str:
-    """What the binding is compiled against besides its own sources: torch's ABI changes with torch, CPython's with Python."""
-    import torch
-    return (f"nvq binding for torch {torch.__version__} {torch.version.git_version} "
-            f"cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}")
-
-
-def binding_fits(path: str) -> bool:
-    """Whether the binding at `path` carries the tag of the torch and Python that run now."""
-    with open(path, "rb") as f:
-        return binding_tag().encode() + b"\0" in f.read()
 
 
 def build_binding(force: bool = False) -> str:
